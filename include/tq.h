@@ -388,6 +388,107 @@ TQ_API tq_status tq_decode_attention_noalloc(const tq_cache* cache, const void* 
                                              int max_blocks_per_seq, const int32_t* lens, float sm_scale,
                                              float* out, int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------- */
+/* 8-bit paged cache (e4m3 codes, a scale for each block and head)         */
+/* ---------------------------------------------------------------------- */
+
+/* A second cache beside the rotated sub-byte one, for layers that do not
+ * stand fewer bits and for caches that other programs read: keys and values
+ * are held as 8-bit floating codes (e4m3: 4 bits of exponent, 3 of fraction,
+ * largest value 448, no infinity) with one scale for each block of block_size
+ * tokens, KV head and side.
+ *   codes   device uint8 [num_blocks, num_kv_heads, 2, block_size, d], side 0
+ *           the keys, side 1 the values
+ *   scales  device fp32  [num_blocks, num_kv_heads, 2], powers of two
+ * A stored value is code * scale.
+ *
+ * The ragged calls take a batch of sequences packed one behind the other: rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of the packed tensors (device int32
+ * [batch + 1], not decreasing, cu_tokens[batch] <= num_tokens) are sequence
+ * b's positions start[b], start[b] + 1, .. (device int32 [batch]); position p
+ * lies in block block_table[b * max_blocks_per_seq + p / block_size], slot
+ * p % block_size.  A sequence may have no rows; rows before cu_tokens[0] and
+ * from cu_tokens[batch] on belong to no sequence: they are not read, and
+ * output rows there are left as they were.  A block id outside the pool, a
+ * position past the block table and a negative start or length set
+ * TQ_FLAG_BAD_SLOT; those positions are skipped.  All sizes and positions on
+ * the device may change between replays of a captured call. */
+typedef struct tq_fp8_cache tq_fp8_cache;
+
+/* Describe a cache over caller-owned codes and scales (16-byte aligned, on the
+ * current CUDA device, which later calls must find current).  Nothing is
+ * allocated on the device and nothing needs to be cleared: a block's scale and
+ * codes are read only where positions of the sequence were written before.
+ * Supported: d = 128, block_size 16, 32, 64 or 128, at most 2^31 rows of codes
+ * (num_blocks * num_kv_heads * 2 * block_size). */
+TQ_API tq_status tq_fp8_cache_create(void* pool, float* scales, int64_t num_blocks, int block_size, int num_kv_heads,
+                                     int d, tq_fp8_cache** out);
+TQ_API void tq_fp8_cache_free(tq_fp8_cache* cache);
+
+/* Quantise new keys and values into the cache.  K and V: device, num_tokens
+ * rows of [num_kv_heads, d] of `dtype`; element (t, h, j) at t * token_stride
+ * + h * head_stride + j (strides in elements, >= 0, every row of d elements on
+ * a 16-byte boundary), so slices of a fused projection are taken as they are.
+ * For every block that new rows of a sequence fall into, each KV head, keys
+ * and values apart:
+ *   e     = the least exponent >= -120 with max |x| <= 448 * 2^e over the new
+ *           rows' finite elements; if the block holds earlier positions of the
+ *           sequence (start[b] inside the block), the larger of that and the
+ *           block's present exponent
+ *   scale = 2^e; new codes = x / scale rounded to e4m3 (nearest, ties to even)
+ *   codes of earlier positions move to the new scale the same way, which is
+ *           exact but for codes that become subnormal (below 2^-6)
+ * Slots behind the last new position keep their bytes; the scale of a block
+ * that starts with new rows does not depend on what was there.  An infinity is
+ * stored as the largest code of its sign and a NaN as 0, and both set
+ * TQ_FLAG_NONFINITE; they do not enter the maximum.  Every block is written by
+ * one group of warps: the same bytes on every run.  Two sequences of a call
+ * that write into the same block race. */
+TQ_API tq_status tq_fp8_write(const tq_fp8_cache* cache, const void* K, const void* V, tq_dtype dtype,
+                              int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                              int64_t v_head_stride, int64_t num_tokens, int batch, const int32_t* cu_tokens,
+                              const int32_t* start, const int32_t* block_table, int max_blocks_per_seq,
+                              int32_t* dev_status, void* stream);
+
+/* Read positions back as dense rows: K and V (device, contiguous [num_tokens,
+ * num_kv_heads, d] of `dtype`, 16-byte aligned) receive code * scale rounded
+ * to the type (nearest, ties to even).  Rows of skipped positions are left as
+ * they were. */
+TQ_API tq_status tq_fp8_read(const tq_fp8_cache* cache, void* K, void* V, tq_dtype dtype, int64_t num_tokens, int batch,
+                             const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table,
+                             int max_blocks_per_seq, int32_t* dev_status, void* stream);
+
+/* Attention of one query token per sequence over its first lens[b] positions:
+ *   out[b, hq] = sum_t softmax_t(sm_scale <q[b, hq], K^_t>) V^_t,  t < lens[b],
+ * with K^, V^ the stored values of KV head hq / (num_q_heads / num_kv_heads).
+ * q: device, `dtype` TQ_BF16 or TQ_F16 (TQ_F32 returns TQ_ERR_UNSUPPORTED),
+ * strided like K above; out: device, contiguous [batch, num_q_heads, d] of the
+ * same type, 16-byte aligned.  lens: device int32 [batch]; a row that attends
+ * to nothing (a length of zero, or every position skipped) is zero.  Slots
+ * behind a sequence's end may hold any bytes.  num_q_heads is a multiple of
+ * num_kv_heads, at most 128 times it.  sm_scale: positive and finite.
+ * workspace: device, 256-byte aligned, at least
+ * tq_fp8_decode_workspace_bytes(...) bytes, zero-filled once before its first
+ * use; each call leaves its counters at zero again.  Two calls in flight at
+ * once, replays of captured ones among them, must not share a workspace. */
+TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* cache, int batch, int num_q_heads);
+TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_seq_stride,
+                                         int64_t q_head_stride, int batch, int num_q_heads, const int32_t* block_table,
+                                         int max_blocks_per_seq, const int32_t* lens, float sm_scale, void* out,
+                                         void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Causal attention of the new tokens of a ragged batch, whose keys and values
+ * are in the cache already (tq_fp8_write first): the query row of position p
+ * attends over positions 0 .. p.  q and out as for the decode call, with rows
+ * [num_tokens, num_q_heads, d] packed like K and V; workspace likewise, with
+ * tq_fp8_prefill_workspace_bytes(...). */
+TQ_API size_t tq_fp8_prefill_workspace_bytes(const tq_fp8_cache* cache, int64_t num_tokens, int batch, int num_q_heads);
+TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype,
+                                          int64_t q_token_stride, int64_t q_head_stride, int64_t num_tokens, int batch,
+                                          int num_q_heads, const int32_t* cu_tokens, const int32_t* start,
+                                          const int32_t* block_table, int max_blocks_per_seq, float sm_scale, void* out,
+                                          void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 /* Whether code on the current device can read and write the memory at p:
  * memory of this device, managed memory, or page-locked host memory mapped
  * into the device's address space at the same address (under unified

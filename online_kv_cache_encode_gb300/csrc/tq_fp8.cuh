@@ -1,0 +1,66 @@
+// Device helpers of the 8-bit paged cache.
+#pragma once
+
+#include "tq_decode_impl.cuh"
+#include "tq_fp8.h"
+
+namespace tq {
+
+// 2^e for -126 <= e <= 127, and the exponent of a power of two.
+__device__ __forceinline__ float fp8_pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int fp8_exp_of(float s) { return ((__float_as_int(s) >> 23) & 0xFF) - 127; }
+
+// The least e >= kFp8MinExp with amax <= 448 * 2^e, for a finite amax >= 0:
+// amax = 1.f * 2^x against 448 = 1.75 * 2^8.
+__device__ __forceinline__ int fp8_exponent(float amax) {
+    const int bits = __float_as_int(amax);
+    const int e = (bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0);
+    return e < kFp8MinExp ? kFp8MinExp : e;
+}
+
+// Two fp32 values to two e4m3 codes (nearest, ties to even; lo in the low byte).
+__device__ __forceinline__ uint32_t fp8_cvt2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes (low 16 bits) to two fp16 values; exact.
+__device__ __forceinline__ uint32_t fp8_to_half2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+__device__ __forceinline__ float2 fp8_to_float2(uint32_t codes) {
+    const uint32_t h = fp8_to_half2(codes);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ int fp8_clamp_cu(const int32_t* cu, int i, int64_t num_tokens) {
+    const int v = __ldg(cu + i);
+    return v < 0 ? 0 : (v > num_tokens ? (int)num_tokens : v);
+}
+
+// Work units of a ragged batch, without a prefix sum: sequence b owns the unit
+// numbers from base(b) = cu[b] / step + 2 b up to base(b + 1).  That many,
+// n / step + 2 at least for its n tokens, covers the blocks of `step` positions
+// its tokens touch, wherever they start; the rest of its numbers stay idle.
+// Finds the sequence of unit u (the last b with base(b) <= u) by probing 32
+// places at a time; the whole warp calls it.
+__device__ __forceinline__ int fp8_seq_of_unit(const int32_t* cu, int batch, int64_t num_tokens, int64_t u, int shift) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int i = lo + lane * step;
+        const bool in = lane == 0 || (i < hi && (int64_t)(fp8_clamp_cu(cu, i, num_tokens) >> shift) + 2 * (int64_t)i <= u);
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+        lo += (31 - __clz((int)m)) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+__host__ __device__ __forceinline__ int64_t fp8_units(int64_t num_tokens, int batch, int shift) {
+    return (num_tokens >> shift) + 2 * (int64_t)batch;
+}
+
+}  // namespace tq

@@ -1,0 +1,75 @@
+// Internal declarations of the 8-bit paged cache (e4m3 codes, one power-of-two
+// scale per block, KV head and side).
+#pragma once
+
+#include <cstdint>
+
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr int kFp8MinExp = -120;   // exponent of the scale of a block of zeros
+constexpr int kFp8MaxGroup = 128;  // query heads per KV head
+
+// Pool: codes [num_blocks][hkv][2: K, V][bs][128], scales [num_blocks][hkv][2].
+struct Fp8Geometry {
+    uint8_t* pool;
+    float* scales;
+    int64_t num_blocks;
+    int hkv;
+    int bs;        // tokens of a block: 16, 32, 64 or 128
+    int bs_shift;  // log2(bs)
+    int num_sms;
+};
+
+// The tokens of a ragged batch: sequence b's rows cu[b] .. cu[b + 1] - 1 of the
+// packed tensors are its positions start[b] ..; block_table [batch][max_blocks].
+struct Fp8Batch {
+    int batch;
+    int64_t num_tokens;  // rows of the packed tensors
+    const int32_t* cu;
+    const int32_t* start;
+    const int32_t* block_table;
+    int max_blocks;
+};
+
+struct Fp8WriteArgs {
+    Fp8Geometry g;
+    Fp8Batch b;
+    const void* K;
+    const void* V;
+    int dtype;
+    int64_t k_token, k_head, v_token, v_head;  // strides in elements
+    int32_t* status;
+};
+struct Fp8ReadArgs {
+    Fp8Geometry g;
+    Fp8Batch b;
+    void* K;
+    void* V;
+    int dtype;
+    int32_t* status;
+};
+struct Fp8AttnArgs {
+    Fp8Geometry g;
+    Fp8Batch b;
+    const int32_t* lens;  // decode: one query row per sequence at position lens[b] - 1
+    const void* q;
+    int dtype;
+    int64_t q_token, q_head;  // strides in elements
+    int hq, group;
+    float sm_scale_log2;
+    void* out;  // [rows][hq][128], q's type
+    int32_t* status;
+};
+
+int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
+int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
+int launch_fp8_attn_simple(const Fp8AttnArgs& a, void* stream);
+
+}  // namespace tq
+
+struct tq_fp8_cache {
+    tq::Fp8Geometry g;
+    int device;
+};

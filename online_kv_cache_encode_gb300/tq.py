@@ -47,6 +47,14 @@ SIGNATURES = {
     "tq_octopus_codebook": (_I, [_I, _I, _I, _P]),
     "tq_prefill_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
     "tq_prefill_attention": (_I, [_P, _P, _I, _I, _I, _P, _I, _I, _F, _P, _P, _SZ, _P, _P]),
+    "tq_fp8_cache_create": (_I, [_P, _P, _I64, _I, _I, _I, ctypes.POINTER(_P)]),
+    "tq_fp8_cache_free": (None, [_P]),
+    "tq_fp8_write": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I, _P, _P]),
+    "tq_fp8_read": (_I, [_P, _P, _P, _I, _I64, _I, _P, _P, _P, _I, _P, _P]),
+    "tq_fp8_decode_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "tq_fp8_decode_attention": (_I, [_P, _P, _I, _I64, _I64, _I, _I, _P, _I, _P, _F, _P, _P, _SZ, _P, _P]),
+    "tq_fp8_prefill_workspace_bytes": (_SZ, [_P, _I64, _I, _I]),
+    "tq_fp8_prefill_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _P, _I, _F, _P, _P, _SZ, _P, _P]),
     "tq_device_accessible": (_I, [_P, ctypes.POINTER(_I)]),
     "tq_test_stall_waits": (None, [_I64]),
     "tq_selftest_tcgen05": (_I, [_P, _P, _P, _P, _P]),
@@ -372,3 +380,144 @@ def octopus_codebook(d: int, bits: int, kind: int) -> np.ndarray:
     out = np.empty(1 << bits, dtype=np.float64)
     _check(lib().tq_octopus_codebook(d, bits, kind, out.ctypes.data_as(ctypes.c_void_p)))
     return out
+
+
+class Fp8Cache:
+    """An 8-bit paged KV cache on the current CUDA device: e4m3 codes and one
+    power-of-two scale for each block, KV head and side (tq_fp8_cache_create).
+
+    pool: uint8 [num_blocks * num_kv_heads * 2 * block_size * d] and scales: fp32
+    [num_blocks, num_kv_heads, 2], allocated here unless given.
+
+    A ragged batch is given as cu_tokens int32 [B + 1], start int32 [B] and
+    block_table int32 [B, max_blocks], all on the device: rows cu_tokens[b] ..
+    cu_tokens[b + 1] - 1 of the packed tensors are positions start[b] .. of
+    sequence b.
+    """
+
+    def __init__(self, num_blocks: int, num_kv_heads: int, block_size: int = 16, d: int = 128,
+                 pool: torch.Tensor | None = None, scales: torch.Tensor | None = None, device="cuda"):
+        self.num_blocks, self.hkv, self.bs, self.d = num_blocks, num_kv_heads, block_size, d
+        if pool is None:
+            pool = torch.zeros(num_blocks * num_kv_heads * 2 * block_size * d, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.ones((num_blocks, num_kv_heads, 2), dtype=torch.float32, device=pool.device)
+        assert pool.dtype == torch.uint8 and pool.is_contiguous()
+        assert pool.numel() >= num_blocks * num_kv_heads * 2 * block_size * d
+        assert scales.dtype == torch.float32 and scales.is_contiguous() and scales.device == pool.device
+        assert scales.numel() >= num_blocks * num_kv_heads * 2
+        self.pool, self.scales = pool, scales
+        self._h = ctypes.c_void_p()
+        with torch.cuda.device(pool.device):
+            _check(lib().tq_fp8_cache_create(_ptr(pool), _ptr(scales), num_blocks, block_size, num_kv_heads, d,
+                                             ctypes.byref(self._h)))
+        self._ws = {}
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value and _lib is not None:
+            _lib.tq_fp8_cache_free(h)
+            self._h = None
+
+    def _batch(self, cu_tokens, start, block_table) -> int:
+        B = start.numel()
+        dev = self.pool.device
+        assert cu_tokens.dtype == torch.int32 and cu_tokens.is_contiguous() and cu_tokens.numel() == B + 1
+        assert start.dtype == torch.int32 and start.is_contiguous()
+        assert block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
+        assert block_table.is_contiguous()
+        assert cu_tokens.device == dev and start.device == dev and block_table.device == dev
+        return B
+
+    def _rows(self, x, heads):
+        """The token and head strides of rows [T, heads, d] (0 where there is one row only)."""
+        assert x.device == self.pool.device and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == self.d
+        assert x.stride(2) == 1
+        return (x.stride(0) if x.shape[0] > 1 else 0), (x.stride(1) if heads > 1 else 0)
+
+    def _workspace(self, kind, nbytes, stream) -> torch.Tensor:
+        # one for each stream, so that calls on two streams may overlap; a call
+        # that is being captured gets its own, cleared by each replay
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.pool.device)
+        ws = self._ws.get((kind, stream))
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.pool.device)
+            self._ws[(kind, stream)] = ws
+        return ws
+
+    def write(self, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
+              block_table: torch.Tensor, status: torch.Tensor | None = None) -> None:
+        """Quantise K, V ([T, num_kv_heads, d], f32/bf16/f16, any token and head strides) into the cache."""
+        B = self._batch(cu_tokens, start, block_table)
+        ks, vs = self._rows(K, self.hkv), self._rows(V, self.hkv)
+        assert K.shape[0] == V.shape[0] and K.dtype == V.dtype
+        with torch.cuda.device(self.pool.device):
+            _check(lib().tq_fp8_write(self._h, _ptr(K), _ptr(V), _dtype_code(K), *ks, *vs, K.shape[0], B, _ptr(cu_tokens), _ptr(start), _ptr(block_table),
+                                      block_table.shape[1], _ptr(status), _stream()))
+
+    def read(self, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
+             dtype: torch.dtype = torch.bfloat16, out: tuple | None = None, status: torch.Tensor | None = None):
+        """The stored keys and values of a ragged batch of positions: two [num_tokens, num_kv_heads, d] tensors
+        (`out`, or new ones).  Rows that belong to no sequence are not written."""
+        B = self._batch(cu_tokens, start, block_table)
+        if out is None:
+            shape = (num_tokens, self.hkv, self.d)
+            out = (torch.empty(shape, dtype=dtype, device=self.pool.device),
+                   torch.empty(shape, dtype=dtype, device=self.pool.device))
+        K, V = out
+        for x in (K, V):
+            self._rows(x, self.hkv)
+            assert x.shape[0] == num_tokens and x.dtype == dtype and x.is_contiguous()
+        with torch.cuda.device(self.pool.device):
+            _check(lib().tq_fp8_read(self._h, _ptr(K), _ptr(V), _dtype_code(K), num_tokens, B, _ptr(cu_tokens),
+                                     _ptr(start), _ptr(block_table), block_table.shape[1], _ptr(status), _stream()))
+        return K, V
+
+    def _attend_args(self, q, sm_scale, out):
+        assert q.dim() == 3
+        strides = self._rows(q, q.shape[1])
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(self.d)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        assert out.device == q.device and out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous()
+        return float(sm_scale), out, strides
+
+    def decode(self, q: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, sm_scale: float | None = None,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               status: torch.Tensor | None = None) -> torch.Tensor:
+        """q: [B, Hq, d] (bf16/f16, any strides of its first two dimensions); lens: int32 [B] -> out [B, Hq, d]
+        of q's type.  A workspace is kept for each stream unless one is given."""
+        sm_scale, out, strides = self._attend_args(q, sm_scale, out)
+        B, hq, _ = q.shape
+        dev = self.pool.device
+        assert block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
+        assert block_table.is_contiguous() and lens.dtype == torch.int32 and lens.numel() == B and lens.is_contiguous()
+        assert block_table.device == dev and lens.device == dev
+        with torch.cuda.device(dev):
+            s = _stream()
+            if workspace is None:
+                workspace = self._workspace("decode", lib().tq_fp8_decode_workspace_bytes(self._h, B, hq), s)
+            _check(lib().tq_fp8_decode_attention(self._h, _ptr(q), _dtype_code(q), *strides, B, hq,
+                                                 _ptr(block_table), block_table.shape[1], _ptr(lens), sm_scale,
+                                                 _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), s))
+        return out
+
+    def prefill(self, q: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor,
+                sm_scale: float | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+        """Causal attention of a ragged batch's new tokens (q: [T, Hq, d]; their keys and values written before)
+        -> out [T, Hq, d] of q's type.  Rows that belong to no sequence are not written."""
+        B = self._batch(cu_tokens, start, block_table)
+        sm_scale, out, strides = self._attend_args(q, sm_scale, out)
+        T, hq, _ = q.shape
+        with torch.cuda.device(self.pool.device):
+            s = _stream()
+            if workspace is None:
+                workspace = self._workspace("prefill", lib().tq_fp8_prefill_workspace_bytes(self._h, T, B, hq), s)
+            _check(lib().tq_fp8_prefill_attention(self._h, _ptr(q), _dtype_code(q), *strides, T, B, hq,
+                                                  _ptr(cu_tokens), _ptr(start), _ptr(block_table),
+                                                  block_table.shape[1], sm_scale, _ptr(out), _ptr(workspace),
+                                                  workspace.numel(), _ptr(status), s))
+        return out
