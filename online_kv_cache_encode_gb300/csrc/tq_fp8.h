@@ -2,6 +2,8 @@
 // scale per block, KV head and side).
 #pragma once
 
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "tq_internal.h"
@@ -65,11 +67,16 @@ struct Fp8AttnArgs {
 
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
+// The pool as rows of 128 codes: the tensor map whose boxes are one block's keys (or values) of a head.
+bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g);
+size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group);
+int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
 int launch_fp8_attn_simple(const Fp8AttnArgs& a, void* stream);
 
 }  // namespace tq
 
 struct tq_fp8_cache {
     tq::Fp8Geometry g;
-    int device;
+    int device;       // -1: made without one
+    CUtensorMap map;
 };

@@ -1,5 +1,7 @@
 // Host side of the 8-bit paged cache: argument checks, the cache descriptor
 // and the calls that launch its kernels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -84,6 +86,26 @@ tq_status check_attn(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64
 
 }  // namespace
 
+namespace tq {
+
+bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)g.num_blocks * g.hkv * 2 * g.bs};
+    const cuuint64_t strides[1] = {(cuuint64_t)kHeadDim};
+    const cuuint32_t box[2] = {(cuuint32_t)kHeadDim, (cuuint32_t)g.bs};
+    const cuuint32_t estr[2] = {1, 1};
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+               map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tq
+
 extern "C" {
 
 TQ_API tq_status tq_fp8_cache_create(void* pool, float* scales, int64_t num_blocks, int block_size, int num_kv_heads,
@@ -115,6 +137,9 @@ TQ_API tq_status tq_fp8_cache_create(void* pool, float* scales, int64_t num_bloc
         cudaGetLastError();
         c->device = -1;
         c->g.num_sms = 0;
+    } else if (!fp8_tensor_map(&c->map, c->g)) {
+        delete c;
+        return fail(TQ_ERR_CUDA, "making the pool's tensor map failed");
     }
     *out = c;
     return TQ_OK;
@@ -172,7 +197,7 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* c, void* K, void* V, tq_dtype d
 
 TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* c, int batch, int num_q_heads) {
     if (!c || batch <= 0 || num_q_heads <= 0 || num_q_heads % c->g.hkv) return 0;
-    return 256;
+    return fp8_decode_workspace(c->g, batch, num_q_heads / c->g.hkv);
 }
 
 TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64_t q_seq_stride,
@@ -200,7 +225,7 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* c, const void* q, t
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     a.out = out;
     a.status = dev_status;
-    const int e = launch_fp8_attn_simple(a, stream);
+    const int e = launch_fp8_decode(a, c->map, workspace, stream);
     return e ? cuda_fail((cudaError_t)e, "decode launch") : TQ_OK;
 }
 
