@@ -67,8 +67,10 @@ struct Fp8AttnArgs {
 
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
-// The pool as rows of 128 codes: the tensor map whose boxes are one block's keys (or values) of a head.
+// The pool as rows of 128 codes: the tensor map whose boxes are one
+// block's keys (or values) of a head, or both where blocks have 16 tokens.
 bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g);
+bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_blocks);  // tiles are counted in 32 bits
 size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group);
 int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
 int launch_fp8_attn_simple(const Fp8AttnArgs& a, void* stream);

@@ -60,28 +60,41 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, ui
 __device__ constexpr uint32_t idesc_f8(int n, bool mn) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (mn ? (3u << 15) : 0u);
 }
-// Rows of 128 bytes in the 128-byte swizzle read MN-major: 8-row groups 1 KB apart along K.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (64ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Rows of 128 bytes in the 128-byte swizzle, 8-row groups `sbo` bytes apart: K-major as they are, or read MN-major,
+// where 128 e4m3 values fill the one atom along M (its leading offset is not used).
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t sbo) { return tc::smem_desc_sw128(saddr, sbo); }
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar)
         : "memory");
 }
+// Whether the phase of the given parity is over; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Floats in the order of signed integers.
-__device__ __forceinline__ int order_key(float x) {
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7FFFFFFF);
+__device__ __forceinline__ float warp_max(float x) {  // NaN is ignored
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
-__device__ __forceinline__ float order_val(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
-
 template <int C>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t* r) {
     if constexpr (C == 4)
@@ -102,23 +115,22 @@ __device__ __forceinline__ void tmem_ready(uint32_t* r) {  // registers are defi
 }
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Reduces C values of every lane over the warp; lane l gets the result of value l % C.
-template <int C, bool MAX>
-__device__ __forceinline__ float reduce_lanes(float (&v)[C]) {
+// Sums C values of every lane over the warp; lane l gets the sum of value l % C.
+template <int C>
+__device__ __forceinline__ float sum_lanes(float (&v)[C]) {
     const int lane = threadIdx.x & 31;
-    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
     for (int w = C / 2; w >= 1; w /= 2) {  // halve the values, keep those of this lane's half
         const bool up = lane & w;
 #pragma unroll
         for (int i = 0; i < w; ++i) {
             const float mine = up ? v[i + w] : v[i], other = up ? v[i] : v[i + w];
-            v[i] = op(mine, __shfl_xor_sync(0xFFFFFFFFu, other, w));
+            v[i] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, w);
         }
     }
     float x = v[0];
 #pragma unroll
-    for (int w = C; w < 32; w *= 2) x = op(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+    for (int w = C; w < 32; w *= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, w);
     return x;
 }
 
@@ -138,14 +150,16 @@ struct DecLayout {
     static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales [16 each]
     static constexpr int okm = meta + kStages * 2 * kPagesMax * 4;  // per stage: pages there, largest value exponent
     static constexpr int mult = okm + kStages * 8;          // per query buffer: [GP]
-    static constexpr int top = mult + QB * GP * 4;          // [3][GP] maxima as ordered ints
-    static constexpr int sums = top + 3 * GP * 4;           // [8 warps][GP]
+    static constexpr int top = (mult + QB * GP * 4 + 15) / 16 * 16;  // [2][8 warps][GP] maxima
+    static constexpr int sums = top + 2 * 8 * GP * 4;       // [8 warps][GP]
     static constexpr int bars = (sums + 8 * GP * 4 + 7) / 8 * 8;
-    static constexpr int nbars = 2 * kStages + 6 + 2 * QB + 1;
+    static constexpr int nbars = 3 * kStages + 6 + 2 * QB + 1;
     static constexpr int misc = bars + 8 * nbars;           // tmem address, last-arrival word
     static constexpr int total = misc + 16;
     static constexpr int smem = total + 1024;               // the base is rounded up to 1 KB
     static constexpr int tmem = 6 * N <= 128 ? 128 : 6 * N <= 256 ? 256 : 512;
+    static_assert(p % 1024 == 0 && q % 1024 == 0 && q_bytes % 1024 == 0, "swizzled rows and 16-byte pieces");
+    static_assert(meta % 16 == 0 && top % 16 == 0 && bars % 8 == 0 && misc % 8 == 0, "vector accesses");
     static_assert(smem <= kSmemLimit, "decode does not fit in shared memory");
 };
 
@@ -159,7 +173,7 @@ struct DecArgs {
     long long stall_cycles;
 };
 
-template <typename T, int NT, int GP>
+template <typename T, int NT, int GP, bool PAIRED>
 __global__ void __launch_bounds__(kDecThreads, 1)
 fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
     using L = DecLayout<NT, GP>;
@@ -170,12 +184,15 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
     const Fp8Geometry& g = A.a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return sb + L::bars + 8 * i; };
-    constexpr int bFull = 0, bEmpty = kStages, bS = 2 * kStages, bP = bS + 2, bO = bP + 2, bQ = bO + 2, bQe = bQ + L::QB,
-                  bNever = bQe + L::QB;
+    // a tile landed, its stage free again, its scales stored; scores, weights and outputs of a tile; queries stored,
+    // and read; one that nothing arrives on (the wait-timeout test hook)
+    constexpr int bF = 0, bE = kStages, bM = 2 * kStages, bS = 3 * kStages, bP = bS + 2, bO = bP + 2, bQ = bO + 2,
+                  bQe = bQ + L::QB, bNever = bQe + L::QB;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar(bFull + i), 2);
-            mbar_init(bar(bEmpty + i), 1);
+            mbar_init(bar(bF + i), 2);
+            mbar_init(bar(bE + i), 1);
+            mbar_init(bar(bM + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(bS + i), 1);
@@ -189,9 +206,9 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         mbar_init(bar(bNever), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 8 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     if (warp == 9) tc::tmem_alloc<L::tmem>(sb + L::misc);
-    int* top_s = reinterpret_cast<int*>(sm + L::top);
-    for (int i = tid; i < 3 * GP; i += kDecThreads) top_s[i] = INT_MIN;
+    float* top_s = reinterpret_cast<float*>(sm + L::top);
     // columns behind NT * GP: query rows and weights of zero, never written again
     for (int i = tid; i < L::QB * L::q_bytes / 4; i += kDecThreads) reinterpret_cast<uint32_t*>(sm + L::q)[i] = 0;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -210,24 +227,25 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         return n < 0 ? 0 : min(n, cap);
     };
     auto tiles = [&](int len) { return max(1, (len + kTile - 1) / kTile); };  // an empty sequence has one, all masked
-    int64_t total = 0;
+    // totals stay below 2^31 (the host checks the largest possible)
+    int total = 0;
     for (int b = lane; b < B; b += 32) total += tiles(length(b));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    total *= HS;
-    const int64_t runs = min((int64_t)gridDim.x, total);
-    const int64_t t0 = (int64_t)blockIdx.x * total / runs, t1 = ((int64_t)blockIdx.x + 1) * total / runs;
-    const bool work = (int64_t)blockIdx.x < runs;
+    total = __reduce_add_sync(0xFFFFFFFFu, total) * HS;
+    const int runs = min((int)gridDim.x, total), cta = (int)blockIdx.x;
+    const int each = total / runs, more = total - each * runs;  // the first `more` runs have a tile more
+    const int t0 = cta * each + min(cta, more), t1 = t0 + each + (cta < more ? 1 : 0);
+    auto run_of = [&](int t) { return t < more * (each + 1) ? t / (each + 1) : more + (t - more * (each + 1)) / each; };
+    const bool work = cta < runs;
     Walk w0{0, 0, 0, 1, 0};
     if (work) {  // the sequence that tile t0 lies in
-        int64_t before = 0;
+        int before = 0;
         for (int b0 = 0;; b0 += 32) {
-            const int b = b0 + lane;
-            const int n = b < B ? tiles(length(b)) : 0;
-            int64_t inc = n;
+            const int b = b0 + lane, len = b < B ? length(b) : 0;
+            const int n = b < B ? tiles(len) : 0;
+            int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
                 if (lane >= o) inc += y;
             }
             const unsigned past = __ballot_sync(0xFFFFFFFFu, (before + inc) * HS > t0);
@@ -235,15 +253,15 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 const int l = past ? __ffs((int)past) - 1 : 31;
                 w0.b = b0 + l;
                 w0.nt = __shfl_sync(0xFFFFFFFFu, n, l);
+                w0.len = __shfl_sync(0xFFFFFFFFu, len, l);
                 before += __shfl_sync(0xFFFFFFFFu, inc, l) - w0.nt;
                 break;
             }
             before += __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
-        w0.len = length(w0.b);
-        const int64_t rem = t0 - before * HS;
-        w0.hs = (int)(rem / w0.nt);
-        w0.ti = (int)(rem - (int64_t)w0.hs * w0.nt);
+        const int rem = t0 - before * HS;
+        w0.hs = rem / w0.nt;
+        w0.ti = rem - w0.hs * w0.nt;
     }
     auto next_item = [&](Walk& w) {
         w.ti = 0;
@@ -260,6 +278,13 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         if (!bad && !mbar_wait(bar(i), parity)) bad = true;
     };
     const int PT = kTile >> g.bs_shift;  // pages of a tile
+    // A stage.  With blocks of 16 tokens (PAIRED) a page's keys and values, 4 KB that lie together in the pool, come in one
+    // copy, page by page: the tensor cores then take the 8-row groups 4 KB apart, the first halves of the 16 pages
+    // and then the second ones, and the tile's tokens go in that order everywhere.  Larger blocks have copies of 4 KB
+    // and more for each side: all keys, then all values.  (A copy costs about 75 cycles to issue: 32 of them a tile
+    // took as long as the tile's bytes.)
+    constexpr uint32_t sbo = PAIRED ? 4096 : 1024;
+    constexpr uint32_t k_half = PAIRED ? 1024 : kSide / 2, v_base = PAIRED ? 2048 : kSide;
     // block id of page `pg` of the tile, or -1
     auto page_id = [&](const Walk& w, int pg) {
         const int64_t i = (int64_t)w.ti * PT + pg;
@@ -270,61 +295,103 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
 
     if (!work) {
         // fewer tiles than CTAs
-    } else if (warp == 8) {
-        // ================= TMA: lanes 0-15 the pages of even tiles, 16-31 of odd ones =================
-        const int half = lane >> 4, pg = lane & 15;
-        const uint32_t bytes = (uint32_t)g.bs * kHeadDim;
+    } else if (warp == 8 || warp == 10) {
+        // ================= TMA: a quarter of the lanes per tile, a lane per copy =================
+        const int quarter = lane >> 3, second = warp == 10;
+        const int pg = (lane & 7) + (PAIRED && second ? 8 : 0);
+        const uint32_t bytes = PAIRED ? 4096 : (uint32_t)g.bs * kHeadDim;
+        const uint32_t at = (uint32_t)pg * bytes + (!PAIRED && second ? kSide : 0);
         asm volatile("fence.proxy.async.global;" ::: "memory");  // the codes were written by ordinary stores
         Walk w = w0;
-        int64_t t = t0;
-        auto advance = [&]() {
-            if (++w.ti == w.nt) next_item(w);
-            ++t;
+        int t = t0;
+        auto advance = [&](int k) {
+            for (; k > 0; --k, ++t)
+                if (++w.ti == w.nt) next_item(w);
         };
-        if (half) advance();
+        advance(quarter);
         int id = t < t1 ? page_id(w, pg) : -1;
-        const int n = (int)(t1 - t0);
-        for (int u = 0; u < n; u += 2) {
-            const int now = id, h = w.hs / A.nsub;
-            if (now == -2) flag(A.a.status, TQ_FLAG_BAD_SLOT);
-            if (pg == 0 && t < t1 && w.ti == 0 && w.hs == 0) {
-                const int raw_len = __ldg(A.a.lens + w.b);
-                if (raw_len < 0 || raw_len > cap) flag(A.a.status, TQ_FLAG_BAD_SLOT);
-            }
-            advance();
-            advance();
-            id = t < t1 ? page_id(w, pg) : -1;  // of two tiles on, while this one's copies are issued
-            for (int k = 0; k < 2 && u + k < n; ++k) {
+        const int n = t1 - t0;
+        for (int u = 0; u < n; u += 4) {
+            const int now = id, h = w.hs / A.nsub, b = w.b;
+            const bool first = t < t1 && w.ti == 0 && w.hs == 0;
+            advance(4);
+            id = t < t1 ? page_id(w, pg) : -1;  // of four tiles on, while these ones' copies are issued
+            const int row = (int)((((int64_t)max(now, 0) * g.hkv + h) * 2 + (!PAIRED && second)) << g.bs_shift);
+            for (int k = 0; k < 4 && u + k < n; ++k) {
                 const int st = (u + k) % kStages, ph = (u + k) / kStages;
-                if (ph > 0) wait(bEmpty + st, (ph - 1) & 1);
-                const unsigned there = __ballot_sync(0xFFFFFFFFu, half == k && now >= 0);
-                if (lane == 0) mbar_arrive_tx(bar(bFull + st), (uint32_t)__popc(there) * 2 * bytes);
+                const unsigned there = __ballot_sync(0xFFFFFFFFu, quarter == k && now >= 0);
+                if (ph > 0) wait(bE + st, (ph - 1) & 1);
+                if (lane == 0) mbar_arrive_tx(bar(bF + st), (uint32_t)__popc(there) * bytes);
                 __syncwarp();
-                if (half == k && now >= 0) {
-                    const int row = (int)((((int64_t)now * g.hkv + h) * 2) << g.bs_shift);
-                    const uint32_t dst = sb + st * 2 * kSide + pg * bytes;
-                    tma_page(dst, &map, row, bar(bFull + st));
-                    tma_page(dst + kSide, &map, row + g.bs, bar(bFull + st));
-                }
+                if (quarter == k && now >= 0) tma_page(sb + st * 2 * kSide + at, &map, row, bar(bF + st));
+            }
+            if (now == -2) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+            if (pg == 0 && !second && first) {
+                const int given = __ldg(A.a.lens + b);
+                if (given < 0 || given > cap) flag(A.a.status, TQ_FLAG_BAD_SLOT);
             }
         }
         // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
-        for (int u = max(0, n - kStages); u < n; ++u) mbar_wait(bar(bFull + u % kStages), (u / kStages) & 1);
+        for (int u = max(0, n - kStages); u < n; ++u) mbar_wait(bar(bF + u % kStages), (u / kStages) & 1);
     } else if (warp == 11) {
-        // ================= scales of the pages =================
+        // ================= queries and scales =================
         Walk w = w0;
-        const int n = (int)(t1 - t0);
-        for (int u = 0; u < n; ++u) {
+        const int n = t1 - t0;
+        bool fresh = true;  // tile u is the item's first here
+        for (int u = 0, i = -1; u < n; ++u) {
             const int st = u % kStages, ph = u / kStages;
+            const int h = w.hs / A.nsub, sub = w.hs - h * A.nsub;
             const int id = lane < 16 ? page_id(w, lane) : -1;
             float2 s = make_float2(0.f, 0.f);
-            if (id >= 0) s = __ldg(reinterpret_cast<const float2*>(g.scales + ((int64_t)id * g.hkv + w.hs / A.nsub) * 2));
-            int e = id >= 0 ? fp8_exp_of(s.y) : -1000;
+            if (id >= 0) s = __ldg(reinterpret_cast<const float2*>(g.scales + ((int64_t)id * g.hkv + h) * 2));
+            if (fresh) {  // the item's queries: NT terms of e4m3, rows in the 128-byte swizzle
+                ++i;
+                const int qb = i % L::QB, use = i / L::QB;
+                const int count = min(GP, A.a.group - sub * GP);
+                const T* q = static_cast<const T*>(A.a.q) + w.b * A.a.q_token +
+                             ((int64_t)h * A.a.group + sub * GP) * A.a.q_head + 4 * lane;
+                uint2 rawq[GP];
+#pragma unroll
+                for (int r = 0; r < GP; ++r)
+                    rawq[r] = r < count ? __ldg(reinterpret_cast<const uint2*>(q + r * A.a.q_head)) : make_uint2(0, 0);
+                if (use > 0) wait(bQe + qb, (use - 1) & 1);
+                float* mult = reinterpret_cast<float*>(sm + L::mult) + qb * GP;
+#pragma unroll
+                for (int r = 0; r < GP; ++r) {
+                    float x[4];
+                    load4(&rawq[r], std::is_same<T, __nv_bfloat16>::value ? TQ_BF16 : TQ_F16, 0, x);
+                    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+                    const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(x[0]) < INFINITY && fabsf(x[1]) < INFINITY &&
+                                                               fabsf(x[2]) < INFINITY && fabsf(x[3]) < INFINITY));
+                    const int e = odd ? 0 : fp8_exponent(top);
+                    const float inv = fp8_pow2(-e);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] *= inv;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const int c = j * GP + r;
+                        const uint32_t lo = fp8_cvt2(x[0], x[1]), hi = fp8_cvt2(x[2], x[3]);
+                        *reinterpret_cast<uint32_t*>(sm + L::q + qb * L::q_bytes + c * 128 +
+                                                     (((lane >> 2) ^ (c & 7)) << 4) + (lane & 3) * 4) = lo | (hi << 16);
+                        const float2 y = fp8_to_float2(lo), z = fp8_to_float2(hi);
+                        x[0] = (x[0] - y.x) * 16.f;
+                        x[1] = (x[1] - y.y) * 16.f;
+                        x[2] = (x[2] - z.x) * 16.f;
+                        x[3] = (x[3] - z.y) * 16.f;
+                    }
+                    // a query that is not finite makes its own row NaN
+                    if (lane == 0) mult[r] = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bQ + qb));
+            }
+            const int e = id >= 0 ? fp8_exp_of(s.y) : -1000;
             int emax = e;
 #pragma unroll
             for (int o = 8; o; o >>= 1) emax = max(emax, __shfl_xor_sync(0xFFFFFFFFu, emax, o));
             const unsigned there = __ballot_sync(0xFFFFFFFFu, id >= 0);
-            if (ph > 0) wait(bEmpty + st, (ph - 1) & 1);
+            if (ph > 0) wait(bE + st, (ph - 1) & 1);
             float* m = reinterpret_cast<float*>(sm + L::meta) + st * 2 * kPagesMax;
             if (lane < 16) {
                 m[lane] = s.x;
@@ -336,102 +403,80 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 o[1] = there ? emax : 0;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(bFull + st));
-            if (++w.ti == w.nt) next_item(w);
-        }
-    } else if (warp == 10) {
-        // ================= queries: NT terms of e4m3, rows in the 128-byte swizzle =================
-        Walk w = w0;
-        int64_t t = t0;
-        for (int i = 0; t < t1; ++i) {
-            const int qb = i % L::QB, use = i / L::QB;
-            const int h = w.hs / A.nsub, sub = w.hs - h * A.nsub;
-            const int count = min(GP, A.a.group - sub * GP);
-            const T* q = static_cast<const T*>(A.a.q) + w.b * A.a.q_token +
-                         ((int64_t)h * A.a.group + sub * GP) * A.a.q_head + 4 * lane;
-            uint2 rawq[GP];
-#pragma unroll
-            for (int r = 0; r < GP; ++r)
-                rawq[r] = r < count ? __ldg(reinterpret_cast<const uint2*>(q + r * A.a.q_head)) : make_uint2(0, 0);
-            if (use > 0) wait(bQe + qb, (use - 1) & 1);
-            float* mult = reinterpret_cast<float*>(sm + L::mult) + qb * GP;
-#pragma unroll
-            for (int r = 0; r < GP; ++r) {
-                float x[4];
-                load4(&rawq[r], std::is_same<T, __nv_bfloat16>::value ? TQ_BF16 : TQ_F16, 0, x);
-                float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-                const bool odd = !(fabsf(x[0]) < INFINITY && fabsf(x[1]) < INFINITY && fabsf(x[2]) < INFINITY &&
-                                   fabsf(x[3]) < INFINITY);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const bool row_odd = __any_sync(0xFFFFFFFFu, odd);
-                const int e = row_odd ? 0 : fp8_exponent(top);
-                const float inv = fp8_pow2(-e);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] *= inv;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int n = j * GP + r;
-                    const uint32_t lo = fp8_cvt2(x[0], x[1]), hi = fp8_cvt2(x[2], x[3]);
-                    *reinterpret_cast<uint32_t*>(sm + L::q + qb * L::q_bytes + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) +
-                                                 (lane & 3) * 4) = lo | (hi << 16);
-                    const float2 a = fp8_to_float2(lo), c = fp8_to_float2(hi);
-                    x[0] = (x[0] - a.x) * 16.f;
-                    x[1] = (x[1] - a.y) * 16.f;
-                    x[2] = (x[2] - c.x) * 16.f;
-                    x[3] = (x[3] - c.y) * 16.f;
-                }
-                // a query that is not finite makes its own row NaN
-                if (lane == 0) mult[r] = row_odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(bQ + qb));
-            t += min((int64_t)(w.nt - w.ti), t1 - t);
-            next_item(w);
+            if (lane == 0) mbar_arrive(bar(bM + st));
+            fresh = w.ti + 1 == w.nt;
+            if (fresh) next_item(w);
+            else ++w.ti;
         }
     } else if (warp == 9) {
         // ================= MMA =================
-        if (lane == 0) {
-            Walk w = w0;
-            int64_t t = t0;
-            int u = 0;
-            auto values = [&](int v) {
-                const int st = v % kStages;
-                wait(bP + (v & 1), (v >> 1) & 1);
+        // Scores of tile u and values of tile v are issued as their operands come: with the cache in HBM the weights
+        // of a tile are ready before the next tile's keys are, with the cache in L2 the other way round.  Scores run
+        // at most one tile ahead (their buffer's last reader has stored the weights of tile u - 2).  The warp stays
+        // together and one lane issues, so that descriptors live in uniform registers.
+        Walk w = w0;
+        const int n = t1 - t0;
+        int u = 0, v = 0;
+        uint32_t su = 0, pu = 0, sv = 0, qb = 0, pq = 0;  // stage and parity of tile u, stage of v, buffer and parity of Q
+        bool fresh = true;                                // tile u is the item's first here
+        long long since = clock64();
+        const uint64_t d_rows = desc_rows(sb, sbo), d_q = desc_rows(sb + L::q, 1024),
+                       d_p = tc::smem_desc(sb + L::p, 128, kTile * 16);
+        const bool issues = elect_one();
+        while (v < n && !bad) {
+            bool did = false;
+            if (v < u && __all_sync(0xFFFFFFFFu, mbar_test(bar(bP + (v & 1)), (v >> 1) & 1))) {
                 tc::fence_after_sync();
-                const uint32_t sv = sb + st * 2 * kSide + kSide, sp = sb + L::p + (v & 1) * L::p_bytes;
+                const uint64_t a = d_rows + (sv * 2 * kSide + v_base) / 16, p = d_p + (v & 1) * (L::p_bytes / 16);
+                const uint32_t d = tmem + 4 * N + (v & 1) * N;
+                if (issues) {
 #pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_f8_ss(tmem + 4 * N + (v & 1) * N, desc_sw128_mn(sv + 4096 * k), tc::smem_desc(sp + 512 * k, 128, kTile * 16),
-                              idesc_f8(N, true), k > 0);
-                tc::commit(bar(bO + (v & 1)));
-                tc::commit(bar(bEmpty + st));
-            };
-            for (int i = 0; t < t1; ++i) {
-                const int qb = i % L::QB;
-                const int n = (int)min((int64_t)(w.nt - w.ti), t1 - t);
-                wait(bQ + qb, (i / L::QB) & 1);
-                const uint32_t sq = sb + L::q + qb * L::q_bytes;
-                for (int j = 0; j < n; ++j, ++u) {
-                    const int st = u % kStages;
-                    wait(bFull + st, (u / kStages) & 1);
-                    tc::fence_after_sync();
+                    for (int k = 0; k < kTile / 32; ++k)
+                        mma_f8_ss(d, a + (PAIRED ? (k >> 2) * 1024 + (k & 3) * 16384 : k * 4096) / 16, p + 32 * k,
+                                  idesc_f8(N, true), k > 0);
+                    tc::commit(bar(bO + (v & 1)));
+                    tc::commit(bar(bE + sv));
+                }
+                __syncwarp();
+                ++v;
+                sv = sv + 1 == kStages ? 0 : sv + 1;
+                did = true;
+            }
+            if (u < n && u <= v + 1 && (!fresh || __all_sync(0xFFFFFFFFu, mbar_test(bar(bQ + qb), pq))) &&
+                __all_sync(0xFFFFFFFFu, mbar_test(bar(bF + su), pu))) {
+                tc::fence_after_sync();
+                const uint64_t q = d_q + qb * (L::q_bytes / 16), a = d_rows + su * 2 * kSide / 16;
+                const uint32_t d = tmem + (u & 1) * 2 * N;
+                fresh = w.ti + 1 == w.nt;
+                const bool last = fresh || u + 1 == n;
+                if (issues) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f8_ss(tmem + ((u & 1) * 2 + m) * N,
-                                      tc::smem_desc_sw128(sb + st * 2 * kSide + m * (kSide / 2) + 32 * k, 1024),
-                                      tc::smem_desc_sw128(sq + 32 * k, 1024), idesc_f8(N, false), k > 0);
+                            mma_f8_ss(d + m * N, a + (m * k_half + 32 * k) / 16, q + 2 * k, idesc_f8(N, false), k > 0);
                     tc::commit(bar(bS + (u & 1)));
-                    if (j == n - 1) tc::commit(bar(bQe + qb));
-                    if (j > 0) values(u - 1);
+                    if (last) tc::commit(bar(bQe + qb));
                 }
-                values(u - 1);  // the item's last: its output is drained before the next one's scores
-                t += n;
-                next_item(w);
+                __syncwarp();
+                ++u;
+                if (++su == kStages) {
+                    su = 0;
+                    pu ^= 1;
+                }
+                if (fresh) {
+                    next_item(w);
+                    if (++qb == L::QB) {
+                        qb = 0;
+                        pq ^= 1;
+                    }
+                } else {
+                    ++w.ti;
+                }
+                did = true;
             }
+            if (did) since = clock64();
+            else if (__any_sync(0xFFFFFFFFu, clock64() - since > kWaitCycles)) bad = true;
         }
         __syncwarp();
     } else {
@@ -439,7 +484,10 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         constexpr int H = GP / 2;  // accumulator columns of a thread
         const int wg = warp >> 2, quad = warp & 3;
         const uint32_t my = tmem + ((uint32_t)(quad * 32) << 16);
-        const int tok = tid;                // token of the tile
+        const int row = tid & 127;
+        const int pg = PAIRED ? row >> 3 : tid >> g.bs_shift;                    // the thread's token: its page,
+        const int tok = PAIRED ? pg * 16 + wg * 8 + (row & 7) : tid;             // its place in the tile,
+        const uint32_t v_row = PAIRED ? pg * 4096 + 2048 + (wg * 8 + (row & 7)) * 128 : kSide + tid * 128;  // its values
         const int dim = quad * 32 + lane;   // output dim
         int* last_s = reinterpret_cast<int*>(sm + L::misc + 8);
         float* sums_s = reinterpret_cast<float*>(sm + L::sums);
@@ -448,21 +496,27 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
             if (empty && tid == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
         }
+        // Weights are 2^(l - ref) against a reference `ref` for each column that moves only when the tile's maximum
+        // leaves [ref - 6, ref + 3/4]: then it goes to 1.5 above that maximum, though not further than 18.5 below the
+        // running one.  So 2^8 times a weight stays below 448, a tile far below the running maximum keeps the bits of
+        // its own weights, and what still lies deeper (2^-14 of a weight unit, 2^-40 of the largest weight) does not
+        // count.  Lane l watches columns 2 (l % (GP / 2)) and the next; sums and accumulators follow the reference,
+        // the latter held 2^-20 small, so that its largest fall leaves them where they would be without it.
+        constexpr int LP = GP / 2;
+        const int mine = lane % LP;
         Walk w = w0;
-        int64_t t = t0;
+        int t = t0;
         int u = 0;
         for (int i = 0; t < t1; ++i) {
             const int qb = i % L::QB;
-            const int n = (int)min((int64_t)(w.nt - w.ti), t1 - t);
-            float m[GP], sum[GP], acc[H], mult[GP], pa[H], pb[H];
+            const int n = min(w.nt - w.ti, t1 - t);
+            float ref[GP], sum[GP], acc[H], mult[GP], fac[H], vs = 0.f;
+            float lref[2] = {0.f, 0.f}, lrun[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < GP; ++k) {
-                m[k] = -INFINITY;
-                sum[k] = 0.f;
-            }
+            for (int k = 0; k < GP; ++k) ref[k] = sum[k] = 0.f;
 #pragma unroll
             for (int k = 0; k < H; ++k) acc[k] = 0.f;
-            auto take_output = [&](int v) {  // acc = acc * pa + O(v) * pb
+            auto take_output = [&](int v) {  // acc += O(v) * vs
                 wait(bO + (v & 1), (v >> 1) & 1);
                 tc::fence_after_sync();
                 __syncwarp();
@@ -475,7 +529,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     float x = __uint_as_float(o[(NT - 1) * H + k]);
 #pragma unroll
                     for (int j = NT - 2; j >= 0; --j) x = fmaf(x, 0.0625f, __uint_as_float(o[j * H + k]));
-                    acc[k] = fmaf(acc[k], pa[k], x * pb[k]);
+                    acc[k] = fmaf(x, vs, acc[k]);
                 }
             };
             wait(bQ + qb, (i / L::QB) & 1);
@@ -483,57 +537,88 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             for (int k = 0; k < GP; ++k) mult[k] = reinterpret_cast<const float*>(sm + L::mult)[qb * GP + k];
             for (int j = 0; j < n; ++j, ++u) {
                 const int st = u % kStages;
-                wait(bFull + st, (u / kStages) & 1);
+                wait(bM + st, (u / kStages) & 1);
                 const float* me = reinterpret_cast<const float*>(sm + L::meta) + st * 2 * kPagesMax;
                 const int* okm = reinterpret_cast<const int*>(sm + L::okm) + 2 * st;
-                const int pg = tok >> g.bs_shift;
                 const bool there = ((okm[0] >> pg) & 1) && (w.ti + j) * kTile + tok < w.len;
-                const float ks = me[pg], vr = me[16 + pg], vscale = fp8_pow2(okm[1]);
+                const float ks = me[pg], vr = me[16 + pg] * kPScale;
+                const float vs_new = fp8_pow2(okm[1]) * (1.f / kPScale / 1048576.f);
                 wait(bS + (u & 1), (u >> 1) & 1);
                 tc::fence_after_sync();
                 __syncwarp();
                 uint32_t s[N];
                 tmem_ld<NT * GP>(my + ((u & 1) * 2 + wg) * N, s);
                 tmem_ready<NT * GP>(s);
-                float l[GP], x[GP];
+                float l[GP];
+                float* top = top_s + (u & 1) * 8 * GP;
+                {
+                    const uint64_t k16 = f2_pack(0.0625f, 0.0625f), ks2 = f2_pack(ks, ks);
 #pragma unroll
-                for (int k = 0; k < GP; ++k) {
-                    float y = __uint_as_float(s[(NT - 1) * GP + k]);
+                    for (int k = 0; k < GP; k += 2) {
+                        uint64_t y = f2_pack(__uint_as_float(s[(NT - 1) * GP + k]), __uint_as_float(s[(NT - 1) * GP + k + 1]));
 #pragma unroll
-                    for (int q = NT - 2; q >= 0; --q) y = fmaf(y, 0.0625f, __uint_as_float(s[q * GP + k]));
-                    l[k] = there ? y * (mult[k] * ks) : -INFINITY;
-                    x[k] = l[k];
-                }
-                // the tile's maximum of every column
-                const float best = reduce_lanes<GP, true>(x);
-                int* top = top_s + (u % 3) * GP;
-                if (lane < GP) atomicMax(top + lane, order_key(best));
-                if (!there) {  // a weight of zero against whatever the slot holds
-                    const uint32_t v = sb + st * 2 * kSide + kSide + tok * kHeadDim;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + 16 * c), "r"(0) : "memory");
-                }
-                soft_barrier();
-                // for the tile after the next: its last readers have passed this barrier, its writers come after the next
-                if (tid < GP) top_s[((u + 2) % 3) * GP + tid] = INT_MIN;
-                if (j == 0 && tid == 0) mbar_arrive(bar(bQe + qb));  // everybody has read the multipliers
-                float na[H], nb[H];
-#pragma unroll
-                for (int k = 0; k < GP; ++k) {
-                    const float mt = order_val(top[k]);
-                    const float mn = fmaxf(m[k], mt), ref = mn == -INFINITY ? 0.f : mn;
-                    const float al = ex2(m[k] - ref), be = ex2(mt - ref);
-                    m[k] = mn;
-                    const float p = ex2(l[k] - (mt == -INFINITY ? 0.f : mt));
-                    sum[k] = fmaf(sum[k], al, p * be);
-                    x[k] = there ? p * (vr * kPScale) : 0.f;
-                    if (k / H == 0 && wg == 0) {
-                        na[k % H] = al;
-                        nb[k % H] = be * (1.f / kPScale) * vscale;
+                        for (int q = NT - 2; q >= 0; --q)
+                            y = f2_fma(y, k16, f2_pack(__uint_as_float(s[q * GP + k]), __uint_as_float(s[q * GP + k + 1])));
+                        f2_unpack(f2_mul(y, f2_mul(f2_pack(mult[k], mult[k + 1]), ks2)), l[k], l[k + 1]);
                     }
-                    if (k / H == 1 && wg == 1) {
-                        na[k % H] = al;
-                        nb[k % H] = be * (1.f / kPScale) * vscale;
+                }
+                if (!there)
+#pragma unroll
+                    for (int k = 0; k < GP; ++k) l[k] = -INFINITY;
+                // the tile's maximum of every column
+                float best[GP];
+#pragma unroll
+                for (int k = 0; k < GP; ++k) best[k] = warp_max(l[k]);
+                if (lane == 0)
+#pragma unroll
+                    for (int k = 0; k < GP; k += 4)
+                        *reinterpret_cast<float4*>(top + warp * GP + k) = make_float4(best[k], best[k + 1], best[k + 2], best[k + 3]);
+                soft_barrier();
+                if (j == 0 && tid == 0) mbar_arrive(bar(bQe + qb));  // everybody has read the multipliers
+                float2 tile = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+                for (int y = 0; y < 8 * LP / 32; ++y) {
+                    const float2 x = *reinterpret_cast<const float2*>(top + (lane / LP + y * (32 / LP)) * GP + 2 * mine);
+                    tile.x = fmaxf(tile.x, x.x);
+                    tile.y = fmaxf(tile.y, x.y);
+                }
+#pragma unroll
+                for (int o = LP; o < 32; o <<= 1) {
+                    tile.x = fmaxf(tile.x, __shfl_xor_sync(0xFFFFFFFFu, tile.x, o));
+                    tile.y = fmaxf(tile.y, __shfl_xor_sync(0xFFFFFFFFu, tile.y, o));
+                }
+                lrun[0] = fmaxf(lrun[0], tile.x);
+                lrun[1] = fmaxf(lrun[1], tile.y);
+                const float to0 = fmaxf(tile.x + 1.5f, lrun[0] - 18.5f), to1 = fmaxf(tile.y + 1.5f, lrun[1] - 18.5f);
+                const bool move0 = tile.x > lref[0] + 0.75f || (tile.x < lref[0] - 6.f && to0 < lref[0]);
+                const bool move1 = tile.y > lref[1] + 0.75f || (tile.y < lref[1] - 6.f && to1 < lref[1]);
+                // the same in every warp; a column without tokens (its maximum is -inf) stays
+                const bool moved = __any_sync(0xFFFFFFFFu, (move0 && to0 > -INFINITY) || (move1 && to1 > -INFINITY));
+                if (moved) {
+                    if (move0 && to0 > -INFINITY) lref[0] = to0;
+                    if (move1 && to1 > -INFINITY) lref[1] = to1;
+#pragma unroll
+                    for (int k = 0; k < GP; ++k) {
+                        const float to = __shfl_sync(0xFFFFFFFFu, lref[k & 1], k >> 1);
+                        // (before the column's first token there is nothing to scale: any finite factor does)
+                        const float f = ex2(fminf(ref[k] - to, 100.f));
+                        ref[k] = to;
+                        sum[k] *= f;
+                        if (k / H == wg) fac[k % H] = f;
+                    }
+                }
+                float x[GP];
+                {
+                    const uint64_t vr2 = f2_pack(vr, vr);
+#pragma unroll
+                    for (int k = 0; k < GP; k += 2) {
+                        float a, b;
+                        f2_unpack(f2_sub(f2_pack(l[k], l[k + 1]), f2_pack(ref[k], ref[k + 1])), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        const uint64_t p = f2_pack(a, b);
+                        f2_unpack(f2_add(f2_pack(sum[k], sum[k + 1]), p), sum[k], sum[k + 1]);
+                        f2_unpack(f2_mul(p, vr2), x[k], x[k + 1]);
                     }
                 }
                 // the weights' terms: byte n of the token's 16-column rows
@@ -546,34 +631,39 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     for (int k = 0; k < GP; k += 4) {
                         const uint32_t lo = fp8_cvt2(x[k], x[k + 1]), hi = fp8_cvt2(x[k + 2], x[k + 3]);
                         word[(q * GP + k) / 4] = lo | (hi << 16);
-                        if (q + 1 < NT) {
+                        if (q + 1 < NT) {  // (x - h) * 16 = 16 x - 16 h, both exact
+                            const uint64_t m16 = f2_pack(-16.f, -16.f), p16 = f2_pack(16.f, 16.f);
                             const float2 a = fp8_to_float2(lo), c = fp8_to_float2(hi);
-                            x[k] = (x[k] - a.x) * 16.f;
-                            x[k + 1] = (x[k + 1] - a.y) * 16.f;
-                            x[k + 2] = (x[k + 2] - c.x) * 16.f;
-                            x[k + 3] = (x[k + 3] - c.y) * 16.f;
+                            f2_unpack(f2_fma(f2_pack(a.x, a.y), m16, f2_mul(f2_pack(x[k], x[k + 1]), p16)), x[k], x[k + 1]);
+                            f2_unpack(f2_fma(f2_pack(c.x, c.y), m16, f2_mul(f2_pack(x[k + 2], x[k + 3]), p16)), x[k + 2], x[k + 3]);
                         }
                     }
-                const uint32_t sp = sb + L::p + (u & 1) * L::p_bytes + tok * 16;
+                const uint32_t sp = sb + L::p + (u & 1) * L::p_bytes + tid * 16;
 #pragma unroll
                 for (int k = 0; k < N / 16; ++k)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sp + k * kTile * 16), "r"(word[4 * k]),
                                  "r"(word[4 * k + 1]), "r"(word[4 * k + 2]), "r"(word[4 * k + 3])
                                  : "memory");
+                if (!there) {  // the token's weights are 0, but its slot may hold NaN codes
+                    wait(bF + st, (u / kStages) & 1);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sb + st * 2 * kSide + v_row + 16 * c), "r"(0)
+                                     : "memory");
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bP + (u & 1)));
                 if (j > 0) take_output(u - 1);
+                vs = vs_new;
+                if (moved)
 #pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    pa[k] = na[k];
-                    pb[k] = nb[k];
-                }
+                    for (int k = 0; k < H; ++k) acc[k] *= fac[k];
             }
             take_output(u - 1);
             // ---- the item's end ----
-            const float part_sum = reduce_lanes<GP, false>(sum);
+            const float part_sum = sum_lanes<GP>(sum);
             if (lane < GP) sums_s[warp * GP + lane] = part_sum;
             soft_barrier();
             float tot[H];
@@ -591,72 +681,85 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             const int count = min(GP, A.a.group - sub * GP);
             const int64_t row0 = (int64_t)w.b * A.a.hq + (int64_t)h * A.a.group + sub * GP;
             T* out = static_cast<T*>(A.a.out) + row0 * kHeadDim;
-            const int64_t a0 = t - w.ti, a1 = a0 + w.nt;  // the item's tiles in the flat list
+            const int a0 = t - w.ti, a1 = a0 + w.nt;  // the item's tiles in the flat list
             if (a0 >= t0 && a1 <= t1) {
 #pragma unroll
                 for (int k = 0; k < H; ++k)
                     if (wg * H + k < count && !empty)
-                        out[(wg * H + k) * kHeadDim + dim] = (T)(tot[k] == 0.f ? 0.f : acc[k] / tot[k]);
+                        out[(wg * H + k) * kHeadDim + dim] = (T)(tot[k] == 0.f ? 0.f : acc[k] * (1048576.f / tot[k]));
                 soft_barrier();
             } else {
                 float* part = A.partials + ((int64_t)blockIdx.x * 2 + (a0 >= t0 ? 1 : 0)) * kPartFloats;
-                float mm[H];
-#pragma unroll
-                for (int k = 0; k < H; ++k) mm[k] = wg ? m[H + k] : m[k];
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
                     part[(wg * H + k) * kHeadDim + dim] = empty ? 0.f : acc[k];
-                    if (dim == 0) {
-                        part[16 * kHeadDim + 2 * (wg * H + k)] = empty ? -INFINITY : mm[k];
+                    if (dim == 0) {  // (a column without tokens has a sum of 0: its reference does not count)
+                        part[16 * kHeadDim + 2 * (wg * H + k)] = empty || tot[k] == 0.f ? -INFINITY : wg ? ref[H + k] : ref[k];
                         part[16 * kHeadDim + 2 * (wg * H + k) + 1] = empty ? 0.f : tot[k];
                     }
                 }
-                const int c0 = (int)(((a0 + 1) * runs - 1) / total), c1 = (int)((a1 * runs - 1) / total);
-                __threadfence();
+                const int c0 = run_of(a0), c1 = run_of(a1 - 1);
                 soft_barrier();
                 if (tid == 0) {
+                    __threadfence();
                     unsigned* c = A.counters + (int64_t)w.b * HS + w.hs;
-                    const unsigned before = atomicAdd(c, 1u);
-                    const bool last = before == (unsigned)(c1 - c0);
+                    const bool last = atomicAdd(c, 1u) == (unsigned)(c1 - c0);
                     if (last) *c = 0u;
                     *last_s = last;
                     __threadfence();
                 }
                 soft_barrier();
                 if (*last_s) {
-                    // join the runs' partials in their order, one warp per query row
+                    // join the runs' partials in their order, one warp per query row: lane c holds the weight of run c
+                    auto of = [&](int c) { return A.partials + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kPartFloats; };
                     for (int r = warp; r < count; r += 8) {
-                        auto of = [&](int c) {
-                            return A.partials + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kPartFloats;
-                        };
-                        float mx = -INFINITY;
-                        for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(of(c) + 16 * kHeadDim + 2 * r));
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                        const float ref = mx == -INFINITY ? 0.f : mx;
+                        float mx = -INFINITY, all = 0.f;
                         float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                        float all = 0.f;
                         for (int cb = c0; cb <= c1; cb += 32) {
-                            float wt = 0.f, sl = 0.f;
-                            if (cb + lane <= c1) {
-                                const float* ml = of(cb + lane) + 16 * kHeadDim + 2 * r;
-                                wt = ex2(__ldcg(ml) - ref);
-                                sl = __ldcg(ml + 1) * wt;
-                            }
                             const int nc = min(32, c1 - cb + 1);
-#pragma unroll 8
-                            for (int c = 0; c < nc; ++c) {
-                                const float f = __shfl_sync(0xFFFFFFFFu, wt, c);
-                                all += __shfl_sync(0xFFFFFFFFu, sl, c);
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(of(cb + c) + r * kHeadDim) + lane);
-                                o4.x = fmaf(v.x, f, o4.x);
-                                o4.y = fmaf(v.y, f, o4.y);
-                                o4.z = fmaf(v.z, f, o4.z);
-                                o4.w = fmaf(v.w, f, o4.w);
+                            float2 ml = make_float2(-INFINITY, 0.f);
+                            if (lane < nc) ml = __ldcg(reinterpret_cast<const float2*>(of(cb + lane) + 16 * kHeadDim) + r);
+                            float4 v[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                v[c] = c < nc ? __ldcg(reinterpret_cast<const float4*>(of(cb + c) + r * kHeadDim) + lane)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                            float mb = ml.x;
+#pragma unroll
+                            for (int o = 16; o; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
+                            const float mn = fmaxf(mx, mb), ref = mn == -INFINITY ? 0.f : mn, al = ex2(mx - ref);
+                            const float wt = ex2(ml.x - ref);
+                            float sl = ml.y * wt;
+                            mx = mn;
+#pragma unroll
+                            for (int o = 16; o; o >>= 1) sl += __shfl_xor_sync(0xFFFFFFFFu, sl, o);
+                            all = fmaf(all, al, sl);
+                            o4.x *= al;
+                            o4.y *= al;
+                            o4.z *= al;
+                            o4.w *= al;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (half) {
+                                    if (nc <= 16) break;
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c)
+                                        v[c] = 16 + c < nc
+                                                   ? __ldcg(reinterpret_cast<const float4*>(of(cb + 16 + c) + r * kHeadDim) + lane)
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    const float f = __shfl_sync(0xFFFFFFFFu, wt, 16 * half + c);
+                                    o4.x = fmaf(v[c].x, f, o4.x);
+                                    o4.y = fmaf(v[c].y, f, o4.y);
+                                    o4.z = fmaf(v[c].z, f, o4.z);
+                                    o4.w = fmaf(v[c].w, f, o4.w);
+                                }
                             }
                         }
-                        const float inv = all == 0.f ? 0.f : 1.f / all;
-                        T y[4] = {(T)(o4.x * inv), (T)(o4.y * inv), (T)(o4.z * inv), (T)(o4.w * inv)};
+                        const float inv = all == 0.f ? 0.f : 1048576.f / all;
+                        alignas(8) T y[4] = {(T)(o4.x * inv), (T)(o4.y * inv), (T)(o4.z * inv), (T)(o4.w * inv)};
                         *reinterpret_cast<uint2*>(out + r * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(y);
                     }
                 }
@@ -675,9 +778,9 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
     }
 }
 
-template <typename T, int NT, int GP>
+template <typename T, int NT, int GP, bool PAIRED>
 int launch(const DecArgs& d, const CUtensorMap& map, int grid, cudaStream_t s) {
-    auto kern = fp8_decode_kernel<T, NT, GP>;
+    auto kern = fp8_decode_kernel<T, NT, GP, PAIRED>;
     static int done[64] = {};
     const cudaError_t e = ensure_smem_limit(kern, DecLayout<NT, GP>::smem, done);
     if (e != cudaSuccess) return (int)e;
@@ -692,7 +795,17 @@ size_t counter_bytes(int batch, int hkv, int group) {
     return ((size_t)batch * hkv * ((group + gp - 1) / gp) * sizeof(unsigned) + 255) / 256 * 256;
 }
 
+int64_t most_tiles(const Fp8Geometry& g, int batch, int group, int max_blocks) {
+    const int gp = part_of(group);
+    const int64_t items = (int64_t)batch * g.hkv * ((group + gp - 1) / gp), per = ((int64_t)max_blocks * g.bs + kTile - 1) / kTile;
+    return items > INT_MAX ? INT64_MAX : items * per;
+}
+
 }  // namespace
+
+bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_blocks) {
+    return most_tiles(g, batch, group, max_blocks) < INT_MAX;
+}
 
 size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group) {
     return counter_bytes(batch, g.hkv, group) + (size_t)(g.num_sms > 0 ? g.num_sms : 1) * 2 * kPartFloats * sizeof(float);
@@ -706,12 +819,16 @@ int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* worksp
     d.counters = static_cast<unsigned*>(workspace);
     d.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(a.b.batch, a.g.hkv, a.group));
     d.stall_cycles = test_stall_cycles();
-    const int64_t most = (int64_t)a.b.batch * a.g.hkv * d.nsub * (((int64_t)a.b.max_blocks * a.g.bs + kTile - 1) / kTile);
+    const int64_t most = most_tiles(a.g, a.b.batch, a.group, a.b.max_blocks);
     const int grid = (int)(most < a.g.num_sms ? most : a.g.num_sms);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype == TQ_BF16)
-        return gp == 8 ? launch<__nv_bfloat16, 2, 8>(d, map, grid, s) : launch<__nv_bfloat16, 2, 16>(d, map, grid, s);
-    return gp == 8 ? launch<__half, 3, 8>(d, map, grid, s) : launch<__half, 3, 16>(d, map, grid, s);
+    const bool paired = a.g.bs == 16;
+    if (a.dtype == TQ_BF16) {
+        if (gp == 8) return paired ? launch<__nv_bfloat16, 2, 8, true>(d, map, grid, s) : launch<__nv_bfloat16, 2, 8, false>(d, map, grid, s);
+        return paired ? launch<__nv_bfloat16, 2, 16, true>(d, map, grid, s) : launch<__nv_bfloat16, 2, 16, false>(d, map, grid, s);
+    }
+    if (gp == 8) return paired ? launch<__half, 3, 8, true>(d, map, grid, s) : launch<__half, 3, 8, false>(d, map, grid, s);
+    return paired ? launch<__half, 3, 16, true>(d, map, grid, s) : launch<__half, 3, 16, false>(d, map, grid, s);
 }
 
 }  // namespace tq

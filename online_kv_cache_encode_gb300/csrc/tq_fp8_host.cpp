@@ -96,7 +96,8 @@ bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g) {
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)g.num_blocks * g.hkv * 2 * g.bs};
     const cuuint64_t strides[1] = {(cuuint64_t)kHeadDim};
-    const cuuint32_t box[2] = {(cuuint32_t)kHeadDim, (cuuint32_t)g.bs};
+    // blocks of 16 tokens: keys and values, which lie together, in one box
+    const cuuint32_t box[2] = {(cuuint32_t)kHeadDim, (cuuint32_t)(g.bs == 16 ? 32 : g.bs)};
     const cuuint32_t estr[2] = {1, 1};
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
                map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -211,7 +212,10 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* c, const void* q, t
     if (max_blocks_per_seq <= 0) return fail(TQ_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
     tq_status st = check_attn(c, q, dtype, q_seq_stride, q_head_stride, num_q_heads, sm_scale, out, workspace,
                               workspace_bytes, tq_fp8_decode_workspace_bytes(c, batch, num_q_heads));
-    if (st != TQ_OK || (st = check_device(c)) != TQ_OK) return st;
+    if (st != TQ_OK) return st;
+    if (!fp8_decode_counts(c->g, batch, num_q_heads / c->g.hkv, max_blocks_per_seq))
+        return fail(TQ_ERR_UNSUPPORTED, "batch, heads and block table make 2^31 tiles or more");
+    if ((st = check_device(c)) != TQ_OK) return st;
     Fp8AttnArgs a{};
     a.g = c->g;
     a.b = make_batch(batch, batch, nullptr, nullptr, block_table, max_blocks_per_seq);

@@ -406,7 +406,9 @@ class Fp8Cache:
         assert pool.numel() >= num_blocks * num_kv_heads * 2 * block_size * d
         assert scales.dtype == torch.float32 and scales.is_contiguous() and scales.device == pool.device
         assert scales.numel() >= num_blocks * num_kv_heads * 2
+        assert pool.is_cuda
         self.pool, self.scales = pool, scales
+        self._dev, self._sm_scale = pool.get_device(), 1.0 / math.sqrt(d)
         self._h = ctypes.c_void_p()
         with torch.cuda.device(pool.device):
             _check(lib().tq_fp8_cache_create(_ptr(pool), _ptr(scales), num_blocks, block_size, num_kv_heads, d,
@@ -419,89 +421,106 @@ class Fp8Cache:
             _lib.tq_fp8_cache_free(h)
             self._h = None
 
-    def _batch(self, cu_tokens, start, block_table) -> int:
-        B = start.numel()
-        dev = self.pool.device
-        assert cu_tokens.dtype == torch.int32 and cu_tokens.is_contiguous() and cu_tokens.numel() == B + 1
-        assert start.dtype == torch.int32 and start.is_contiguous()
-        assert block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
-        assert block_table.is_contiguous()
-        assert cu_tokens.device == dev and start.device == dev and block_table.device == dev
-        return B
+    # The checks below run on every call of a serving loop: each reads an attribute once, and the device is only
+    # switched where the current one is another.
+    def _away(self) -> bool:
+        return torch._C._cuda_getDevice() != self._dev
+
+    def _int32(self, *tensors) -> bool:
+        dev = self._dev
+        return all(x.dtype is torch.int32 and x.get_device() == dev and x.is_contiguous() for x in tensors)
+
+    def _batch(self, cu_tokens, start, block_table, status):
+        """(batch, max_blocks) of a ragged batch's arguments."""
+        B, mb = block_table.shape
+        assert self._int32(cu_tokens, start, block_table), "int32, contiguous, on the cache's device"
+        assert cu_tokens.numel() == B + 1 and start.numel() == B
+        assert status is None or self._int32(status)
+        return B, mb
 
     def _rows(self, x, heads):
         """The token and head strides of rows [T, heads, d] (0 where there is one row only)."""
-        assert x.device == self.pool.device and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == self.d
-        assert x.stride(2) == 1
-        return (x.stride(0) if x.shape[0] > 1 else 0), (x.stride(1) if heads > 1 else 0)
+        T, h, d = x.shape
+        st, sh, sd = x.stride()
+        assert h == heads and d == self.d and sd == 1 and x.get_device() == self._dev
+        return (st if T > 1 else 0), (sh if h > 1 else 0)
 
-    def _workspace(self, kind, nbytes, stream) -> torch.Tensor:
+    def _workspace(self, kind, key, stream, nbytes) -> torch.Tensor:
         # one for each stream, so that calls on two streams may overlap; a call
         # that is being captured gets its own, cleared by each replay
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.pool.device)
-        ws = self._ws.get((kind, stream))
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.pool.device)
-            self._ws[(kind, stream)] = ws
-        return ws
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return torch.zeros(max(nbytes(self._h, *key), 256), dtype=torch.uint8, device=self.pool.device)
+        held = self._ws.get((kind, stream))
+        if held is None or held[0] != key:
+            need = max(nbytes(self._h, *key), 256)
+            if held is None or held[1].numel() < need:
+                held = (key, torch.zeros(need, dtype=torch.uint8, device=self.pool.device))
+            self._ws[(kind, stream)] = held = (key, held[1])
+        return held[1]
 
     def write(self, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
               block_table: torch.Tensor, status: torch.Tensor | None = None) -> None:
         """Quantise K, V ([T, num_kv_heads, d], f32/bf16/f16, any token and head strides) into the cache."""
-        B = self._batch(cu_tokens, start, block_table)
+        if self._away():
+            with torch.cuda.device(self._dev):
+                return self.write(K, V, cu_tokens, start, block_table, status)
+        B, mb = self._batch(cu_tokens, start, block_table, status)
         ks, vs = self._rows(K, self.hkv), self._rows(V, self.hkv)
-        assert K.shape[0] == V.shape[0] and K.dtype == V.dtype
-        with torch.cuda.device(self.pool.device):
-            _check(lib().tq_fp8_write(self._h, _ptr(K), _ptr(V), _dtype_code(K), *ks, *vs, K.shape[0], B, _ptr(cu_tokens), _ptr(start), _ptr(block_table),
-                                      block_table.shape[1], _ptr(status), _stream()))
+        T, dtype = K.shape[0], K.dtype
+        assert V.shape[0] == T and V.dtype is dtype
+        _check(lib().tq_fp8_write(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], *ks, *vs, T, B,
+                                  cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
+                                  torch._C._cuda_getCurrentRawStream(self._dev)))
 
     def read(self, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
              dtype: torch.dtype = torch.bfloat16, out: tuple | None = None, status: torch.Tensor | None = None):
         """The stored keys and values of a ragged batch of positions: two [num_tokens, num_kv_heads, d] tensors
         (`out`, or new ones).  Rows that belong to no sequence are not written."""
-        B = self._batch(cu_tokens, start, block_table)
+        if self._away():
+            with torch.cuda.device(self._dev):
+                return self.read(cu_tokens, start, block_table, num_tokens, dtype, out, status)
+        B, mb = self._batch(cu_tokens, start, block_table, status)
         if out is None:
-            shape = (num_tokens, self.hkv, self.d)
-            out = (torch.empty(shape, dtype=dtype, device=self.pool.device),
-                   torch.empty(shape, dtype=dtype, device=self.pool.device))
-        K, V = out
-        for x in (K, V):
-            self._rows(x, self.hkv)
-            assert x.shape[0] == num_tokens and x.dtype == dtype and x.is_contiguous()
-        with torch.cuda.device(self.pool.device):
-            _check(lib().tq_fp8_read(self._h, _ptr(K), _ptr(V), _dtype_code(K), num_tokens, B, _ptr(cu_tokens),
-                                     _ptr(start), _ptr(block_table), block_table.shape[1], _ptr(status), _stream()))
+            shape, dev = (num_tokens, self.hkv, self.d), self.pool.device
+            K, V = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            K, V = out
+            for x in out:
+                self._rows(x, self.hkv)
+                assert x.shape[0] == num_tokens and x.dtype is dtype and x.is_contiguous()
+        _check(lib().tq_fp8_read(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], num_tokens, B,
+                                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
+                                 torch._C._cuda_getCurrentRawStream(self._dev)))
         return K, V
 
     def _attend_args(self, q, sm_scale, out):
-        assert q.dim() == 3
-        strides = self._rows(q, q.shape[1])
-        if sm_scale is None:
-            sm_scale = 1.0 / math.sqrt(self.d)
+        T, hq, _ = q.shape
+        strides = self._rows(q, hq)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        assert out.device == q.device and out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous()
-        return float(sm_scale), out, strides
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            assert out.get_device() == self._dev and out.dtype is q.dtype and out.shape == q.shape
+            assert out.is_contiguous()
+        return T, hq, strides, self._sm_scale if sm_scale is None else float(sm_scale), out
 
     def decode(self, q: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, sm_scale: float | None = None,
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                status: torch.Tensor | None = None) -> torch.Tensor:
         """q: [B, Hq, d] (bf16/f16, any strides of its first two dimensions); lens: int32 [B] -> out [B, Hq, d]
         of q's type.  A workspace is kept for each stream unless one is given."""
-        sm_scale, out, strides = self._attend_args(q, sm_scale, out)
-        B, hq, _ = q.shape
-        dev = self.pool.device
-        assert block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
-        assert block_table.is_contiguous() and lens.dtype == torch.int32 and lens.numel() == B and lens.is_contiguous()
-        assert block_table.device == dev and lens.device == dev
-        with torch.cuda.device(dev):
-            s = _stream()
-            if workspace is None:
-                workspace = self._workspace("decode", lib().tq_fp8_decode_workspace_bytes(self._h, B, hq), s)
-            _check(lib().tq_fp8_decode_attention(self._h, _ptr(q), _dtype_code(q), *strides, B, hq,
-                                                 _ptr(block_table), block_table.shape[1], _ptr(lens), sm_scale,
-                                                 _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), s))
+        if self._away():
+            with torch.cuda.device(self._dev):
+                return self.decode(q, block_table, lens, sm_scale, out, workspace, status)
+        B, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
+        rows, mb = block_table.shape
+        assert self._int32(block_table, lens), "int32, contiguous, on the cache's device"
+        assert rows == B and lens.numel() == B and (status is None or self._int32(status))
+        stream = torch._C._cuda_getCurrentRawStream(self._dev)
+        if workspace is None:
+            workspace = self._workspace("decode", (B, hq), stream, lib().tq_fp8_decode_workspace_bytes)
+        _check(lib().tq_fp8_decode_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, B, hq,
+                                             block_table.data_ptr(), mb, lens.data_ptr(), sm_scale, out.data_ptr(),
+                                             workspace.data_ptr(), workspace.nbytes, _ptr(status), stream))
         return out
 
     def prefill(self, q: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor,
@@ -509,15 +528,16 @@ class Fp8Cache:
                 workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
         """Causal attention of a ragged batch's new tokens (q: [T, Hq, d]; their keys and values written before)
         -> out [T, Hq, d] of q's type.  Rows that belong to no sequence are not written."""
-        B = self._batch(cu_tokens, start, block_table)
-        sm_scale, out, strides = self._attend_args(q, sm_scale, out)
-        T, hq, _ = q.shape
-        with torch.cuda.device(self.pool.device):
-            s = _stream()
-            if workspace is None:
-                workspace = self._workspace("prefill", lib().tq_fp8_prefill_workspace_bytes(self._h, T, B, hq), s)
-            _check(lib().tq_fp8_prefill_attention(self._h, _ptr(q), _dtype_code(q), *strides, T, B, hq,
-                                                  _ptr(cu_tokens), _ptr(start), _ptr(block_table),
-                                                  block_table.shape[1], sm_scale, _ptr(out), _ptr(workspace),
-                                                  workspace.numel(), _ptr(status), s))
+        if self._away():
+            with torch.cuda.device(self._dev):
+                return self.prefill(q, cu_tokens, start, block_table, sm_scale, out, workspace, status)
+        B, mb = self._batch(cu_tokens, start, block_table, status)
+        T, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
+        stream = torch._C._cuda_getCurrentRawStream(self._dev)
+        if workspace is None:
+            workspace = self._workspace("prefill", (T, B, hq), stream, lib().tq_fp8_prefill_workspace_bytes)
+        _check(lib().tq_fp8_prefill_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, T, B, hq,
+                                              cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb,
+                                              sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                              _ptr(status), stream))
         return out

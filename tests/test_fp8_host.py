@@ -95,7 +95,8 @@ def test_decode(tq, cache):
         return tq.lib().tq_fp8_decode_attention(h, P(q), dt, *qs, B, hq, P(table), mb, P(lens), sm, P(out), P(ws), nws,
                                                 None, None)
     for k, e in ATTN + [(dict(table=0), "INVALID_ARG"), (dict(lens=0), "INVALID_ARG"), (dict(mb=0), "INVALID_ARG"),
-                        (dict(B=-1), "INVALID_ARG")]:
+                        (dict(B=-1), "INVALID_ARG"), (dict(B=1 << 25, mb=1 << 12), "UNSUPPORTED"),
+                        (dict(B=(1 << 31) - 1, mb=(1 << 31) - 1, nws=1 << 60), "UNSUPPORTED")]:
         assert call(**k) == getattr(tq, "TQ_ERR_" + e), k
     assert call(B=0, q=0) == tq.TQ_OK
     L = tq.lib()
