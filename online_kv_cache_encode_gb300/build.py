@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libtq.so")
 SOURCES = [("tq_host.cpp", [], "tq_host.o"), ("tq_encode.cu", [], "tq_encode.o"), ("tq_decode.cu", [], "tq_decode.o"),
            ("tq_octopus.cu", [], "tq_octopus.o"), ("tq_selftest.cu", [], "tq_selftest.o"),
            ("tq_prefill_tc.cu", [], "tq_prefill_tc.o"), ("tq_fp8_host.cpp", [], "tq_fp8_host.o"),
-           ("tq_fp8.cu", [], "tq_fp8.o"), ("tq_fp8_decode.cu", [], "tq_fp8_decode.o")]
+           ("tq_fp8.cu", [], "tq_fp8.o"), ("tq_fp8_decode.cu", [], "tq_fp8_decode.o"),
+           ("tq_fp8_prefill.cu", [], "tq_fp8_prefill.o")]
 SOURCES += [("tq_inst.cu", [f"-DTQ_KB={kb}"], f"tq_inst_k{kb}.o") for kb in range(1, 9)]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -282,106 +282,4 @@ int launch_fp8_read(const Fp8ReadArgs& a, void* stream) {
     return (int)launch_programmatic(fp8_read_kernel<__half>, grid, block, 0, s, a, shift);
 }
 
-// ---------------------------------------------------------------------------
-// Attention, one warp per query row and head: a lane scores one token at a time
-// over 32 tokens, then the warp adds up their values, four dimensions a lane.
-// ---------------------------------------------------------------------------
-namespace {
-
-template <typename T>
-__global__ void __launch_bounds__(128) fp8_attn_simple_kernel(const Fp8AttnArgs a) {
-    __shared__ float qs[4][kHeadDim];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t item = (int64_t)blockIdx.x * 4 + warp;
-    const int64_t row = item / a.hq;
-    const int hq = (int)(item - row * a.hq), h = hq / a.group;
-    if (row >= a.b.num_tokens) return;
-    int b;
-    int64_t n;  // tokens the row attends to
-    if (a.lens) {
-        b = (int)row;
-        n = a.lens[b];
-    } else {
-        b = 0;
-        while (b + 1 < a.b.batch && a.b.cu[b + 1] <= row) ++b;
-        if (row < a.b.cu[b] || row >= a.b.cu[b + 1]) return;
-        n = (int64_t)a.b.start[b] + (row - a.b.cu[b]) + 1;
-        if (a.b.start[b] < 0) { flag(a.status, TQ_FLAG_BAD_SLOT); n = 0; }
-    }
-    if (n > (int64_t)a.b.max_blocks * a.g.bs) {
-        flag(a.status, TQ_FLAG_BAD_SLOT);
-        n = (int64_t)a.b.max_blocks * a.g.bs;
-    }
-    const T* q = static_cast<const T*>(a.q) + row * a.q_token + hq * a.q_head;
-    bool odd = false;
-    for (int i = lane; i < kHeadDim; i += 32) {
-        odd |= !finite((float)q[i]);
-        qs[warp][i] = (float)q[i] * a.sm_scale_log2;
-    }
-    odd = __any_sync(0xFFFFFFFFu, odd);
-    float m = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t t0 = 0; t0 < n; t0 += 32) {
-        const int64_t t = t0 + lane;
-        int blk = -1;
-        if (t < n) {
-            blk = a.b.block_table[(int64_t)b * a.b.max_blocks + (t >> a.g.bs_shift)];
-            if (blk < 0 || blk >= a.g.num_blocks) { flag(a.status, TQ_FLAG_BAD_SLOT); blk = -1; }
-        }
-        float s = -INFINITY, vs = 0.f;
-        int64_t vrow = 0;
-        if (blk >= 0) {
-            const int64_t page = ((int64_t)blk * a.g.hkv + h) * 2;
-            const int64_t krow = page * a.g.bs + (t & (a.g.bs - 1));
-            const uint2* k = reinterpret_cast<const uint2*>(a.g.pool + krow * kHeadDim);
-            float acc = 0.f;
-            for (int c = 0; c < 16; ++c) {
-                const uint2 w = k[c];
-                const float2 f0 = fp8_to_float2(w.x & 0xFFFFu), f1 = fp8_to_float2(w.x >> 16);
-                const float2 f2 = fp8_to_float2(w.y & 0xFFFFu), f3 = fp8_to_float2(w.y >> 16);
-                const float* qq = &qs[warp][8 * c];
-                acc += qq[0] * f0.x + qq[1] * f0.y + qq[2] * f1.x + qq[3] * f1.y + qq[4] * f2.x + qq[5] * f2.y +
-                       qq[6] * f3.x + qq[7] * f3.y;
-            }
-            s = acc * a.g.scales[page];
-            vs = a.g.scales[page + 1];
-            vrow = krow + a.g.bs;
-        }
-        float mt = s;
-        for (int d = 16; d; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, d));
-        const float mn = fmaxf(m, mt);
-        if (mn == -INFINITY) continue;
-        const float al = exp2f(m - mn);
-        const float p = blk >= 0 ? exp2f(s - mn) : 0.f;
-        m = mn;
-        sum = sum * al + p;
-        for (int k = 0; k < 4; ++k) o[k] *= al;
-        for (int i = 0; i < 32; ++i) {
-            const int bi = __shfl_sync(0xFFFFFFFFu, blk, i);
-            const float pi = __shfl_sync(0xFFFFFFFFu, p * vs, i);
-            const int64_t vr = __shfl_sync(0xFFFFFFFFu, vrow, i);
-            if (bi < 0) continue;
-            const uint32_t w = *(reinterpret_cast<const uint32_t*>(a.g.pool + vr * kHeadDim) + lane);
-            const float2 f0 = fp8_to_float2(w & 0xFFFFu), f1 = fp8_to_float2(w >> 16);
-            o[0] += pi * f0.x; o[1] += pi * f0.y; o[2] += pi * f1.x; o[3] += pi * f1.y;
-        }
-    }
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const float inv = odd ? NAN : m == -INFINITY ? 0.f : 1.f / sum;
-    T* out = static_cast<T*>(a.out) + (row * a.hq + hq) * kHeadDim + 4 * lane;
-    for (int k = 0; k < 4; ++k) out[k] = (T)(o[k] * inv);
-}
-
-}  // namespace
-
-int launch_fp8_attn_simple(const Fp8AttnArgs& a, void* stream) {
-    const int64_t ctas = (a.b.num_tokens * a.hq + 3) / 4;
-    if (ctas > 0x7FFFFFFF) return (int)cudaErrorInvalidConfiguration;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype == TQ_BF16)
-        return (int)launch_programmatic(fp8_attn_simple_kernel<__nv_bfloat16>, dim3((unsigned)ctas), dim3(128), 0, s, a);
-    return (int)launch_programmatic(fp8_attn_simple_kernel<__half>, dim3((unsigned)ctas), dim3(128), 0, s, a);
-}
-
 }  // namespace tq

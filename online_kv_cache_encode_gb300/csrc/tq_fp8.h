@@ -67,18 +67,20 @@ struct Fp8AttnArgs {
 
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
-// The pool as rows of 128 codes: the tensor map whose boxes are one
-// block's keys (or values) of a head, or both where blocks have 16 tokens.
-bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g);
+// The pool as rows of 128 codes: the tensor map whose boxes have `rows` of them.
+bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g, int rows);
 bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_blocks);  // tiles are counted in 32 bits
 size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group);
 int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
-int launch_fp8_attn_simple(const Fp8AttnArgs& a, void* stream);
+bool fp8_prefill_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);  // the grid fits 32 bits
+size_t fp8_prefill_workspace(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);
+int launch_fp8_prefill(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
 
 }  // namespace tq
 
 struct tq_fp8_cache {
     tq::Fp8Geometry g;
     int device;       // -1: made without one
-    CUtensorMap map;
+    CUtensorMap map;   // boxes of a block's keys or values of one head; with blocks of 16 tokens of both
+    CUtensorMap side;  // boxes of a block's keys or values
 };

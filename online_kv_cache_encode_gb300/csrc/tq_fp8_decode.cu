@@ -33,10 +33,9 @@
 #include <cuda_runtime.h>
 
 #include <climits>
-#include <type_traits>
 
 #include "tq_fp8.cuh"
-#include "tq_tcgen05.cuh"
+#include "tq_fp8_tc.cuh"
 
 namespace tq {
 namespace {
@@ -49,52 +48,6 @@ constexpr int kDecWarps = 12;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr float kPScale = 256.f;      // weights are coded as p * 2^8 <= 256
 
-__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// kind::f8f6f4, e4m3 x e4m3 -> fp32, M = 128; bits 15 and 16 read A and B MN-major
-__device__ constexpr uint32_t idesc_f8(int n, bool mn) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (mn ? (3u << 15) : 0u);
-}
-// Rows of 128 bytes in the 128-byte swizzle, 8-row groups `sbo` bytes apart: K-major as they are, or read MN-major,
-// where 128 e4m3 values fill the one atom along M (its leading offset is not used).
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t sbo) { return tc::smem_desc_sw128(saddr, sbo); }
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar)
-        : "memory");
-}
-// Whether the phase of the given parity is over; does not wait.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float warp_max(float x) {  // NaN is ignored
-    float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
 template <int C>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t* r) {
     if constexpr (C == 4)
@@ -359,8 +312,12 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
                 for (int r = 0; r < GP; ++r) {
                     float x[4];
-                    load4(&rawq[r], std::is_same<T, __nv_bfloat16>::value ? TQ_BF16 : TQ_F16, 0, x);
-                    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+                    const float2 q01 = two_floats<T>(rawq[r].x), q23 = two_floats<T>(rawq[r].y);
+                    x[0] = q01.x;
+                    x[1] = q01.y;
+                    x[2] = q23.x;
+                    x[3] = q23.y;
+                    const float top = redux_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
                     const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(x[0]) < INFINITY && fabsf(x[1]) < INFINITY &&
                                                                fabsf(x[2]) < INFINITY && fabsf(x[3]) < INFINITY));
                     const int e = odd ? 0 : fp8_exponent(top);
@@ -568,7 +525,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 // the tile's maximum of every column
                 float best[GP];
 #pragma unroll
-                for (int k = 0; k < GP; ++k) best[k] = warp_max(l[k]);
+                for (int k = 0; k < GP; ++k) best[k] = redux_max(l[k]);
                 if (lane == 0)
 #pragma unroll
                     for (int k = 0; k < GP; k += 4)
@@ -759,8 +716,8 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                             }
                         }
                         const float inv = all == 0.f ? 0.f : 1048576.f / all;
-                        alignas(8) T y[4] = {(T)(o4.x * inv), (T)(o4.y * inv), (T)(o4.z * inv), (T)(o4.w * inv)};
-                        *reinterpret_cast<uint2*>(out + r * kHeadDim + 4 * lane) = *reinterpret_cast<const uint2*>(y);
+                        *reinterpret_cast<uint2*>(out + r * kHeadDim + 4 * lane) =
+                            make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));
                     }
                 }
                 soft_barrier();

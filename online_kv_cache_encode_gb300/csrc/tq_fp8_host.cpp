@@ -88,7 +88,7 @@ tq_status check_attn(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64
 
 namespace tq {
 
-bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g) {
+bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g, int rows) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
@@ -96,8 +96,7 @@ bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g) {
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)g.num_blocks * g.hkv * 2 * g.bs};
     const cuuint64_t strides[1] = {(cuuint64_t)kHeadDim};
-    // blocks of 16 tokens: keys and values, which lie together, in one box
-    const cuuint32_t box[2] = {(cuuint32_t)kHeadDim, (cuuint32_t)(g.bs == 16 ? 32 : g.bs)};
+    const cuuint32_t box[2] = {(cuuint32_t)kHeadDim, (cuuint32_t)rows};
     const cuuint32_t estr[2] = {1, 1};
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
                map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -138,7 +137,7 @@ TQ_API tq_status tq_fp8_cache_create(void* pool, float* scales, int64_t num_bloc
         cudaGetLastError();
         c->device = -1;
         c->g.num_sms = 0;
-    } else if (!fp8_tensor_map(&c->map, c->g)) {
+    } else if (!fp8_tensor_map(&c->map, c->g, block_size == 16 ? 32 : block_size) || !fp8_tensor_map(&c->side, c->g, block_size)) {
         delete c;
         return fail(TQ_ERR_CUDA, "making the pool's tensor map failed");
     }
@@ -234,8 +233,9 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* c, const void* q, t
 }
 
 TQ_API size_t tq_fp8_prefill_workspace_bytes(const tq_fp8_cache* c, int64_t num_tokens, int batch, int num_q_heads) {
-    if (!c || num_tokens <= 0 || num_tokens > INT_MAX || batch <= 0 || num_q_heads <= 0 || num_q_heads % c->g.hkv) return 0;
-    return 256;
+    if (!c || num_tokens <= 0 || num_tokens > INT_MAX || batch <= 0 || num_q_heads <= 0 || num_q_heads % c->g.hkv || num_q_heads / c->g.hkv > kFp8MaxGroup)
+        return 0;
+    return fp8_prefill_workspace(c->g, num_tokens, batch, num_q_heads / c->g.hkv);
 }
 
 TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64_t q_token_stride,
@@ -247,7 +247,10 @@ TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* c, const void* q, 
     if (st != TQ_OK || num_tokens == 0 || batch == 0) return st;
     st = check_attn(c, q, dtype, q_token_stride, q_head_stride, num_q_heads, sm_scale, out, workspace, workspace_bytes,
                     tq_fp8_prefill_workspace_bytes(c, num_tokens, batch, num_q_heads));
-    if (st != TQ_OK || (st = check_device(c)) != TQ_OK) return st;
+    if (st != TQ_OK) return st;
+    if (!fp8_prefill_counts(c->g, num_tokens, batch, num_q_heads / c->g.hkv))
+        return fail(TQ_ERR_UNSUPPORTED, "more query rows than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
     Fp8AttnArgs a{};
     a.g = c->g;
     a.b = make_batch(num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
@@ -260,7 +263,7 @@ TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* c, const void* q, 
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     a.out = out;
     a.status = dev_status;
-    const int e = launch_fp8_attn_simple(a, stream);
+    const int e = launch_fp8_prefill(a, c->side, workspace, stream);
     return e ? cuda_fail((cudaError_t)e, "prefill launch") : TQ_OK;
 }
 

@@ -1,0 +1,682 @@
+// Causal attention of a ragged batch's new tokens over the 8-bit paged cache,
+// on the tensor cores.
+//
+// A unit is 256 query rows of one sequence and KV head (row = token * group +
+// query head in the group), two tiles A and B of 128 rows; a CTA takes a unit,
+// or one of its splits over the tokens, 128 tokens a step:
+//   S [128 rows x 128 tokens] = Q . K^T    kind::f8f6f4
+//   O [128 rows x 128 dims]  += P . V      kind::f16 with bf16 operands
+// K goes to the tensor cores as its codes.  A query row is split into e4m3
+// terms that add up in one accumulator, x = h1 + h2 (+ h3), scaled so that its
+// largest element lies in [224, 448]: 2 terms are a bf16 query's 8 bits (3 an
+// fp16 one's 11), down to steps of 2^-9, 2^-17.8 of the row's largest element.
+// Two passes of fp8 cost what one of bf16 does, and K needs no conversion.
+// V's codes times their block's scale are exact in bf16, and bf16 weights keep
+// their relative precision at any size, so a weight far below a dominating one
+// (or on a block with a small scale) counts with its own bits; fp8 weights in
+// one accumulator would not do that.  Weights round to bf16 (2^-8) for bf16
+// queries; fp16 ones add the remainder as a second bf16 operand (2^-16).
+//
+// Bounds, per 128 tokens and 256 rows: tensor cores 1024 (QK, 2 terms) + 1024
+// (PV) cycles, exponentials 1024 at 32 a cycle, shared memory about 2200 (both
+// operands of QK, V's conversion).  Hence two row tiles that take turns: the
+// tensor cores work on one while the softmax of the other runs, and both use
+// the same K and V.
+//
+// Warps: 0-3 softmax of A, 4-7 of B (thread = row), 8-11 V's conversion, 12
+// TMA, 13 MMA, 14 scales.  Tensor memory: S_A, S_B (their weights overwrite
+// them), O_A, O_B, 128 columns each.  The maximum of a row moves only when a
+// score beats it by more than 8 (log2 units), by a rescale of O in place.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "tq_fp8.cuh"
+#include "tq_fp8_tc.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kRowsPerTile = 128;
+constexpr int kUnitRows = 256;
+constexpr int kTok = 128;                    // tokens of a step
+constexpr int kThreads = 512;
+constexpr int kMetaRing = 4;
+constexpr float kLazyRise = 8.f;
+
+template <int NT>
+struct PreLayout {
+    static constexpr int KS = NT == 2 ? 3 : 2;          // stages of keys
+    static constexpr int q = 0;                         // [2 tiles][NT][128 rows][128 B], 128-byte swizzle
+    static constexpr int k = q + 2 * NT * 16384;        // [KS][128 tokens][128 B], 128-byte swizzle
+    static constexpr int v = k + KS * 16384;            // [2][128 tokens][128 B] codes, 128-byte swizzle
+    static constexpr int vb = v + 2 * 16384;            // [2] bf16 operand: 8 x 8 core matrices, MN-major
+    static constexpr int meta = vb + 2 * 32768;         // [ring]: key scales [8], value scales [8] of 16 tokens each
+    static constexpr int okm = meta + kMetaRing * 64;   // [ring]: groups of 16 tokens that are there
+    static constexpr int bars = okm + kMetaRing * 4 + 16 - kMetaRing * 4 % 16;
+    static constexpr int nbars = 2 + 2 * KS + 4 + 4 + 6 + 2 * kMetaRing + 1;
+    static constexpr int misc = bars + nbars * 8;
+    static constexpr int total = misc + 16;
+    static constexpr int smem = total + 1024;
+    static_assert(k % 1024 == 0 && v % 1024 == 0 && vb % 1024 == 0 && meta % 16 == 0 && bars % 8 == 0, "alignment");
+    static_assert(smem <= kSmemLimit, "prefill does not fit in shared memory");
+};
+// V's operand: 8 tokens x 8 dims core matrices of 128 bytes, token groups 128 bytes apart, dim groups 2048
+constexpr uint32_t kVLbo = 128, kVSbo = 2048;
+
+struct PreArgs {
+    Fp8AttnArgs a;
+    int tpt;              // tokens of a row tile: 128 / group
+    int splits;
+    float* partials;      // [units][hkv][splits][256][128], unnormalised (splits > 1)
+    float2* ml;           // [units][hkv][splits][256] (maximum, sum)
+    long long stall_cycles;
+};
+
+// The sequence of unit u, where sequence b owns the numbers from base(b) = cu[b] / step + b on: enough for its
+// ceil(n / step) units wherever it starts.  The whole warp calls it.
+__device__ __forceinline__ int seq_of(const int32_t* cu, int batch, int64_t num_tokens, int u, int step) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int jump = (hi - lo + 31) >> 5, i = lo + lane * jump;
+        const bool in = lane == 0 || (i < hi && fp8_clamp_cu(cu, i, num_tokens) / step + i <= u);
+        lo += (31 - __clz((int)__ballot_sync(0xFFFFFFFFu, in))) * jump;
+        hi = min(hi, lo + jump);
+    }
+    return lo;
+}
+__host__ __device__ __forceinline__ int64_t pre_units(int64_t num_tokens, int batch, int step) {
+    return num_tokens / step + batch;
+}
+
+// A unit: its sequence, packed rows and positions.
+struct Unit {
+    int b, n, first;   // sequence, its new tokens, the unit's first among them
+    int64_t row0;      // packed row of the sequence's first new token
+    int start;         // its position (a negative one is flagged, its rows attend to nothing)
+    bool live;
+};
+__device__ __forceinline__ Unit find_unit(const Fp8Batch& b, int u, int step) {
+    Unit x;
+    x.b = seq_of(b.cu, b.batch, b.num_tokens, u, step);
+    const int c0 = fp8_clamp_cu(b.cu, x.b, b.num_tokens), c1 = fp8_clamp_cu(b.cu, x.b + 1, b.num_tokens);
+    x.n = c1 - c0;
+    x.row0 = c0;
+    const int64_t first = ((int64_t)u - (c0 / step + x.b)) * step;
+    x.live = first >= 0 && first < x.n;
+    x.first = x.live ? (int)first : 0;
+    x.start = __ldg(b.start + x.b);
+    return x;
+}
+
+__device__ __forceinline__ void pre_sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <typename T, int NT, int NP>  // NP: bf16 operands of the weights
+__global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs A, const __grid_constant__ CUtensorMap map) {
+    using L = PreLayout<NT>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    const Fp8Geometry& g = A.a.g;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto bar = [&](int i) { return sb + L::bars + 8 * i; };
+    // queries of a tile stored; keys landed, free; codes of values landed, free; operand of values stored, free;
+    // scores, weights, output of a row tile; scales stored, free; one that nothing arrives on
+    constexpr int bQ = 0, bK = 2, bKe = bK + L::KS, bV = bKe + L::KS, bVe = bV + 2, bB = bVe + 2, bBe = bB + 2, bS = bBe + 2,
+                  bP = bS + 2, bO = bP + 2, bM = bO + 2, bMe = bM + kMetaRing, bNever = bMe + kMetaRing;
+    static_assert(bNever + 1 == L::nbars, "barriers");
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(bQ + i), 4);
+            mbar_init(bar(bV + i), 1);
+            mbar_init(bar(bVe + i), 4);
+            mbar_init(bar(bB + i), 4);
+            mbar_init(bar(bBe + i), 1);
+            mbar_init(bar(bS + i), 1);
+            mbar_init(bar(bP + i), 4);
+            mbar_init(bar(bO + i), 1);
+        }
+        for (int i = 0; i < L::KS; ++i) {
+            mbar_init(bar(bK + i), 1);
+            mbar_init(bar(bKe + i), 1);
+        }
+        for (int i = 0; i < kMetaRing; ++i) {
+            mbar_init(bar(bM + i), 1);
+            mbar_init(bar(bMe + i), 1);
+        }
+        mbar_init(bar(bNever), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+    if (warp == 13) tc::tmem_alloc<512>(sb + L::misc);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::misc);
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the unit, its row tiles and this split's tokens ----
+    // heads and splits run fastest; the units go from the last back, as those attend to the most tokens
+    const int split = blockIdx.x % A.splits, uh = blockIdx.x / A.splits;
+    const int h = uh % g.hkv;
+    const int u_all = (int)(gridDim.x / A.splits / g.hkv);
+    const int unit = u_all - 1 - uh / g.hkv;
+    const Unit U = find_unit(A.a.b, unit, 2 * A.tpt);
+    const int G = A.a.group;
+    const int64_t cap = (int64_t)A.a.b.max_blocks * g.bs;
+    // tokens that a row tile's last row sees, and how many steps that takes
+    auto steps_of = [&](int x) {
+        const int t0 = U.first + x * A.tpt;
+        if (!U.live || t0 >= U.n) return 0;
+        const int64_t end = U.start < 0 ? 0 : min((int64_t)U.start + min(U.n, t0 + A.tpt), cap);
+        return max(1, (int)((end + kTok - 1) / kTok));
+    };
+    const int nA = steps_of(0), nB = steps_of(1), nt = max(nA, nB);
+    const int s0 = (int)((int64_t)nt * split / A.splits), s1 = (int)((int64_t)nt * (split + 1) / A.splits);
+    const int cnt = s1 - s0;
+    const int cA = min(max(nA - s0, 0), cnt), cB = min(max(nB - s0, 0), cnt);
+    const int64_t slot = ((int64_t)unit * g.hkv + h) * A.splits + split;
+
+    bool bad = false;
+    auto wait = [&](int i, uint32_t parity) {
+        if (!bad && !mbar_wait(bar(i), parity)) bad = true;
+    };
+    // id of the block that holds tokens 16 j .. of step u, or -1 (past the end) or -2 (not in the pool)
+    auto block_of = [&](int u, int j) {
+        const int64_t p = (int64_t)(s0 + u) * kTok + 16 * j;
+        const int64_t end = min((int64_t)U.start + min(U.n, U.first + 2 * A.tpt), cap);
+        if (U.start < 0 || p >= end) return -1;
+        const int id = __ldg(A.a.b.block_table + (int64_t)U.b * A.a.b.max_blocks + (p >> g.bs_shift));
+        return id >= 0 && id < g.num_blocks ? id : -2;
+    };
+
+    if (!U.live) {
+        // no such unit
+    } else if (warp < 8) {
+        // ================= softmax: thread = query row =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int x = warp >> 2;                       // row tile
+        const int r = tid & 127;
+        const int tok = U.first + x * A.tpt + r / G;   // new token of the sequence
+        const bool there = r < A.tpt * G && tok < U.n;
+        const int64_t out_row = (U.row0 + tok) * A.a.hq + (int64_t)h * G + r % G;
+        const int steps = x ? cB : cA;
+        const int64_t pos = (int64_t)U.start + tok;    // attends to tokens 0 .. pos
+        const int64_t pos0 = (int64_t)U.start + U.first + x * A.tpt;  // of the tile's first row
+        const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tS = my + x * 128, tO = my + 256 + x * 128;
+        bool empty = false;
+        if (A.stall_cycles > 0 && (split & 1)) {
+            empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
+            if (empty && r == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
+        }
+        float mult = 0.f;
+        if (steps > 0) {
+            // the row's query in e4m3 terms
+            uint4 raw_q[16];
+            const T* q = static_cast<const T*>(A.a.q) + (U.row0 + tok) * A.a.q_token + ((int64_t)h * G + r % G) * A.a.q_head;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                raw_q[c] = there ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
+            float top = 0.f;
+            bool odd = false;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t w[4] = {raw_q[c].x, raw_q[c].y, raw_q[c].z, raw_q[c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = two_floats<T>(w[k]);
+                    odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            const int e = odd ? 0 : fp8_exponent(top);
+            const float inv = fp8_pow2(-e);
+            mult = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
+            const uint32_t dst = sb + L::q + x * NT * 16384 + r * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {  // 16 elements: one 16-byte piece of every term
+                float y[16];
+                const uint32_t w[8] = {raw_q[2 * c].x,     raw_q[2 * c].y,     raw_q[2 * c].z,     raw_q[2 * c].w,
+                                       raw_q[2 * c + 1].x, raw_q[2 * c + 1].y, raw_q[2 * c + 1].z, raw_q[2 * c + 1].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = two_floats<T>(w[k]);
+                    y[2 * k] = f.x * inv;
+                    y[2 * k + 1] = f.y * inv;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t lo = fp8_cvt2(y[4 * k], y[4 * k + 1]), hi = fp8_cvt2(y[4 * k + 2], y[4 * k + 3]);
+                        o[k] = lo | (hi << 16);
+                        const float2 a = fp8_to_float2(lo), b = fp8_to_float2(hi);
+                        y[4 * k] -= a.x;
+                        y[4 * k + 1] -= a.y;
+                        y[4 * k + 2] -= b.x;
+                        y[4 * k + 3] -= b.y;
+                    }
+                    pre_sts128(dst + j * 16384 + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bQ + x));
+        }
+        float m = -INFINITY;  // the reference: raised only when a score beats it by more than kLazyRise
+        float2 sum2 = make_float2(0.f, 0.f);
+        for (int u = 0; u < steps; ++u) {
+            const int mi = u % kMetaRing;
+            wait(bM + mi, (u / kMetaRing) & 1);
+            const float* ks = reinterpret_cast<const float*>(sm + L::meta + mi * 64);
+            const int ok = *reinterpret_cast<const int*>(sm + L::okm + mi * 4);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[j] = ks[j] * mult;
+                if (f[j] < 1e-37f) f[j] = 1e-37f;  // a masked score of -inf stays one (NaN stays NaN)
+            }
+            const int64_t tile0 = (int64_t)(s0 + u) * kTok;
+            wait(bS + x, u & 1);
+            tc::fence_after_sync();
+            __syncwarp();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+            tc::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::reg_fence(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+            if (ok != 0xFF || tile0 + kTok - 1 > pos0) {  // somebody's mask begins in this tile, or a page is missing
+                const int64_t rest = pos - tile0;
+                const int limit = rest < -1 ? -1 : rest > kTok ? kTok : (int)rest;  // tokens 0 .. limit of the tile
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j > limit || !((ok >> (j >> 4)) & 1)) s[j] = 0xFF800000u;
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // the scales are positive: maximum first, scale after
+                float y = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y = fmaxf(y, __uint_as_float(s[16 * j + k]));
+                mx = fmaxf(mx, y == -INFINITY ? y : y * f[j]);
+            }
+            const bool rise = mx > m + kLazyRise || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, rise)) {
+                const float fac = rise ? ex2(m - mx) : 1.f;
+                if (rise) m = mx;
+                sum2.x *= fac;
+                sum2.y *= fac;
+                if (u > 0) {
+                    wait(bO + x, (u - 1) & 1);  // the output of the step before is complete
+                    tc::fence_after_sync();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16];
+                        tc::ld_32x32b_x16(tO + 16 * c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+                        }
+                        tc::st_32x32b_x16(tO + 16 * c, o);
+                    }
+                    tc::wait_st();
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            const uint64_t neg = f2_pack(-ref, -ref);
+            uint64_t acc = f2_pack(sum2.x, sum2.y), acc2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const int j = 32 * c + k;
+                    const uint64_t fj = f2_pack(f[j >> 4], f[j >> 4]);
+                    float a, b;
+                    // a masked score is -inf: its product with a positive scale too
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), fj, neg), a, b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    if (k & 2) acc = f2_add(acc, f2_pack(a, b));
+                    else acc2 = f2_add(acc2, f2_pack(a, b));
+                    hi[k / 2] = pack_bf16(a, b);
+                    if constexpr (NP == 2)
+                        lo[k / 2] = pack_bf16(a - __uint_as_float(hi[k / 2] << 16), b - __uint_as_float(hi[k / 2] & 0xFFFF0000u));
+                }
+                tc::st_32x32b_x16(tS + 16 * c, hi);
+                if constexpr (NP == 2) tc::st_32x32b_x16(tS + 64 + 16 * c, lo);
+            }
+            acc = f2_add(acc, acc2);
+            f2_unpack(acc, sum2.x, sum2.y);
+            tc::wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bP + x));
+        }
+        // ---- the rows' end ----
+        if (bad && !empty) {
+            flag(A.a.status, TQ_FLAG_TIMEOUT);
+            empty = true;
+        }
+        const float sum = sum2.x + sum2.y;
+        if (steps > 0) {
+            wait(bO + x, (steps - 1) & 1);
+            tc::fence_after_sync();
+            __syncwarp();
+        }
+        if (A.splits == 1) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            T* out = static_cast<T*>(A.a.out) + out_row * kHeadDim;
+            if (steps > 0)
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::ld_32x32b_x32(tO + 32 * c, o);
+                    tc::wait_ld();
+                    tc::reg_fence(o);
+                    if (there && !empty)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float a = sum == 0.f ? 0.f : __uint_as_float(o[k + 2 * i]) * inv;
+                                const float b = sum == 0.f ? 0.f : __uint_as_float(o[k + 2 * i + 1]) * inv;
+                                w[i] = pack_two<T>(a, b);
+                            }
+                            *reinterpret_cast<uint4*>(out + 32 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+        } else {
+            const int64_t at = slot * kUnitRows + x * kRowsPerTile + r;
+            const bool none = steps == 0 || empty || sum == 0.f;
+            A.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : sum);
+            if (steps > 0)
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::ld_32x32b_x32(tO + 32 * c, o);
+                    tc::wait_ld();
+                    tc::reg_fence(o);
+                    if (there && !none)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(A.partials + at * kHeadDim + 32 * c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+        }
+    } else if (warp < 12) {
+        // ================= V: codes to bf16, times the block's scale =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int cw = warp - 8;
+        for (int u = 0; u < cnt; ++u) {
+            const int b = u & 1, mi = u % kMetaRing;
+            wait(bM + mi, (u / kMetaRing) & 1);
+            wait(bV + b, (u >> 1) & 1);
+            if (u > 1) wait(bBe + b, ((u - 2) >> 1) & 1);
+            const int* vs = reinterpret_cast<const int*>(sm + L::meta + mi * 64 + 32);
+            const uint32_t src = sb + L::v + b * 16384, dst = sb + L::vb + b * 32768;
+            // a warp converts 32 tokens: 8 of them by 4 pieces of 16 codes at a time
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+                const int t = cw * 32 + (i >> 1) * 8 + (lane & 7), c = (i & 1) * 4 + (lane >> 3);
+                const uint4 v4 = lds128(src + t * 128 + ((c ^ (t & 7)) << 4));
+                const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+                const int e = vs[t >> 4];  // exponent of the value scale, or INT_MIN where there is no block
+                // e4m3's fields moved into bf16's read as the value times 2^-120 (subnormals too)
+                const int e1 = min(e + 120, 127);
+                const uint32_t f1 = e == INT_MIN ? 0u : (uint32_t)(e1 + 127 > 254 ? 254 : e1 + 127) << 7;
+                const uint32_t m1 = f1 | (f1 << 16);
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = prmt(w[k], 0, 0x1404), z = prmt(w[k], 0, 0x3424);
+                    o[2 * k] = mul_bf16x2((a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), m1);
+                    o[2 * k + 1] = mul_bf16x2((z & 0x80008000u) | ((z & 0x7F007F00u) >> 4), m1);
+                }
+                if (e > 7) {  // 2^(e + 120) is past bf16's range: the rest in a second product
+                    const uint32_t f2 = (uint32_t)(e - 7 + 127) << 7, m2 = f2 | (f2 << 16);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], m2);
+                }
+                const uint32_t at = dst + (2 * c) * kVSbo + (t >> 3) * kVLbo + (t & 7) * 16;
+                pre_sts128(at, o[0], o[1], o[2], o[3]);
+                pre_sts128(at + kVSbo, o[4], o[5], o[6], o[7]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(bB + b));
+                mbar_arrive(bar(bVe + b));
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 12) {
+            // ================= TMA: lanes 0-7 the blocks' keys, 8-15 their values =================
+            const int pages = kTok >> g.bs_shift, pg = lane & 7, side = (lane >> 3) & 1;
+            const uint32_t bytes = (uint32_t)g.bs * kHeadDim;
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // the codes were written by ordinary stores
+            const bool mine = lane < 16 && pg < pages;
+            const int per = g.bs >> 4;  // groups of 16 tokens in a block
+            int id = mine && cnt > 0 ? block_of(0, pg * per) : -1;
+            for (int u = 0; u < cnt; ++u) {
+                const int now = id;
+                id = mine && u + 1 < cnt ? block_of(u + 1, pg * per) : -1;
+                const int row = (int)((((int64_t)max(now, 0) * g.hkv + h) * 2 + side) << g.bs_shift);
+                const unsigned kmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 0), vmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 1);
+                const int ks = u % L::KS;
+                if (u >= L::KS) wait(bKe + ks, (u / L::KS - 1) & 1);
+                if (lane == 0) mbar_arrive_tx(bar(bK + ks), (uint32_t)__popc(kmask) * bytes);
+                __syncwarp();
+                if (now >= 0 && side == 0) tma_page(sb + L::k + ks * 16384 + pg * bytes, &map, row, bar(bK + ks));
+                if (u > 1) wait(bVe + (u & 1), ((u - 2) >> 1) & 1);
+                if (lane == 0) mbar_arrive_tx(bar(bV + (u & 1)), (uint32_t)__popc(vmask) * bytes);
+                __syncwarp();
+                if (now >= 0 && side == 1) tma_page(sb + L::v + (u & 1) * 16384 + pg * bytes, &map, row, bar(bV + (u & 1)));
+                if (now == -2) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+            }
+            if (lane == 0 && (U.start < 0 || (int64_t)U.start + min(U.n, U.first + 2 * A.tpt) > cap)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+            // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
+            for (int u = max(0, cnt - L::KS); u < cnt; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
+            for (int u = max(0, cnt - 2); u < cnt; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
+        } else if (warp == 14) {
+            // ================= scales of every 16 tokens =================
+            for (int u = 0; u < cnt; ++u) {
+                const int mi = u % kMetaRing;
+                const int id = lane < 8 ? block_of(u, lane) : -1;
+                float2 s = make_float2(0.f, 0.f);
+                if (id >= 0) s = __ldg(reinterpret_cast<const float2*>(g.scales + ((int64_t)id * g.hkv + h) * 2));
+                const unsigned ok = __ballot_sync(0xFFFFFFFFu, id >= 0);
+                if (u >= kMetaRing) wait(bMe + mi, (u / kMetaRing - 1) & 1);
+                if (lane < 8) {
+                    // where there is no block any positive scale does: the scores are masked
+                    reinterpret_cast<float*>(sm + L::meta + mi * 64)[lane] = id >= 0 ? s.x : 1.f;
+                    reinterpret_cast<int*>(sm + L::meta + mi * 64 + 32)[lane] = id >= 0 ? fp8_exp_of(s.y) : INT_MIN;
+                }
+                if (lane == 0) *reinterpret_cast<int*>(sm + L::okm + mi * 4) = (int)ok;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bM + mi));
+            }
+        } else if (warp == 13) {
+            // ================= MMA: QK A(u), PV B(u - 1), QK B(u), PV A(u) =================
+            const bool issues = elect_one();
+            const uint64_t d_q = desc_rows(sb + L::q, 1024), d_k = desc_rows(sb + L::k, 1024),
+                           d_v = tc::smem_desc(sb + L::vb, kVLbo, kVSbo);
+            constexpr uint32_t idesc_v = tc::idesc_bf16_f32(128, 128) | (1u << 16);
+            auto scores = [&](int x, int ks) {
+                tc::fence_after_sync();
+                if (issues) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8_ss(tmem + x * 128, d_q + (x * NT + j) * 1024 + 2 * k, d_k + ks * 1024 + 2 * k, idesc_f8(128, false),
+                                      j > 0 || k > 0);
+                    tc::commit(bar(bS + x));
+                }
+                __syncwarp();
+            };
+            auto values = [&](int x, int u) {
+                wait(bB + (u & 1), (u >> 1) & 1);
+                wait(bP + x, u & 1);
+                __syncwarp();
+                tc::fence_after_sync();
+                if (issues) {
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + 64 * j + 8 * k, d_v + (u & 1) * 2048 + 16 * k, idesc_v,
+                                           u > 0 || j > 0 || k > 0);
+                    tc::commit(bar(bO + x));
+                }
+                __syncwarp();
+            };
+            auto release = [&](int u) {  // both tiles' values of step u are issued
+                if (issues) {
+                    tc::commit(bar(bBe + (u & 1)));
+                    tc::commit(bar(bMe + u % kMetaRing));
+                }
+                __syncwarp();
+            };
+            if (cA > 0) wait(bQ, 0);
+            if (cB > 0) wait(bQ + 1, 0);
+            for (int u = 0; u < cnt; ++u) {
+                const int ks = u % L::KS;
+                wait(bK + ks, (u / L::KS) & 1);
+                __syncwarp();
+                if (u < cA) scores(0, ks);
+                if (u > 0) {
+                    if (u - 1 < cB) values(1, u - 1);
+                    release(u - 1);
+                }
+                if (u < cB) scores(1, ks);
+                if (issues) tc::commit(bar(bKe + ks));
+                __syncwarp();
+                if (u < cA) values(0, u);
+            }
+            if (cnt > 0) {
+                if (cnt - 1 < cB) values(1, cnt - 1);
+                release(cnt - 1);
+            }
+        }
+    }
+    if (bad && lane == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 13) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc<512>(tmem);
+    }
+}
+
+// Joins the splits of every row, one warp per row, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_prefill_join_kernel(const PreArgs A) {
+    const int lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = (int)(item % kUnitRows);
+    const int64_t uh = item / kUnitRows;
+    const int h = (int)(uh % A.a.g.hkv), unit = (int)(uh / A.a.g.hkv);
+    if (unit >= pre_units(A.a.b.num_tokens, A.a.b.batch, 2 * A.tpt)) return;
+    const Unit U = find_unit(A.a.b, unit, 2 * A.tpt);
+    const int x = r / kRowsPerTile, rr = r % kRowsPerTile, G = A.a.group;
+    const int tok = U.first + x * A.tpt + rr / G;
+    if (!U.live || rr >= A.tpt * G || tok >= U.n) return;
+    const int64_t at = uh * A.splits * kUnitRows + r;
+    float mx = -INFINITY;
+    for (int s = lane; s < A.splits; s += 32) mx = fmaxf(mx, A.ml[at + (int64_t)s * kUnitRows].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    float all = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < A.splits; ++s) {
+        const float2 ml = A.ml[at + (int64_t)s * kUnitRows];
+        if (ml.y == 0.f) continue;  // nothing there, and nothing stored
+        const float w = ex2(ml.x - ref);
+        const float4 v = *(reinterpret_cast<const float4*>(A.partials + (at + (int64_t)s * kUnitRows) * kHeadDim) + lane);
+        all = fmaf(ml.y, w, all);
+        o4.x = fmaf(v.x, w, o4.x);
+        o4.y = fmaf(v.y, w, o4.y);
+        o4.z = fmaf(v.z, w, o4.z);
+        o4.w = fmaf(v.w, w, o4.w);
+    }
+    const float inv = all == 0.f ? 0.f : 1.f / all;
+    T* out = static_cast<T*>(A.a.out) + ((U.row0 + tok) * A.a.hq + (int64_t)h * G + rr % G) * kHeadDim;
+    *(reinterpret_cast<uint2*>(out) + lane) = make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));
+}
+
+int tokens_per_tile(int group) { return kRowsPerTile / group; }
+
+// Splits over the tokens, where the units alone leave SMs idle.
+int splits_of(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
+    const int step = 2 * tokens_per_tile(group);
+    const int64_t units = ((num_tokens + step - 1) / step + (batch - 1) / 2) * g.hkv;  // about as many as there are
+    const int64_t s = (g.num_sms > 0 ? g.num_sms : 1) / units;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+template <typename T, int NT, int NP>
+int launch(const PreArgs& p, const CUtensorMap& map, int64_t units, cudaStream_t s) {
+    auto kern = fp8_prefill_kernel<T, NT, NP>;
+    static int done[64] = {};
+    cudaError_t e = ensure_smem_limit(kern, PreLayout<NT>::smem, done);
+    if (e != cudaSuccess) return (int)e;
+    e = launch_programmatic(kern, dim3((unsigned)(units * p.a.g.hkv * p.splits)), dim3(kThreads), (size_t)PreLayout<NT>::smem, s, p, map);
+    if (e != cudaSuccess || p.splits == 1) return (int)e;
+    return (int)launch_programmatic(fp8_prefill_join_kernel<T>, dim3((unsigned)(units * p.a.g.hkv * (kUnitRows / 8))), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+bool fp8_prefill_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
+    return pre_units(num_tokens, batch, 2 * tokens_per_tile(group)) * g.hkv * (kUnitRows / 8) < INT_MAX;
+}
+
+size_t fp8_prefill_workspace(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
+    const int splits = splits_of(g, num_tokens, batch, group);
+    if (splits == 1) return 256;
+    const size_t rows = (size_t)pre_units(num_tokens, batch, 2 * tokens_per_tile(group)) * g.hkv * splits * kUnitRows;
+    return rows * (kHeadDim * sizeof(float) + sizeof(float2));
+}
+
+int launch_fp8_prefill(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream) {
+    PreArgs p{};
+    p.a = a;
+    p.tpt = tokens_per_tile(a.group);
+    p.splits = splits_of(a.g, a.b.num_tokens, a.b.batch, a.group);
+    const int64_t units = pre_units(a.b.num_tokens, a.b.batch, 2 * p.tpt);
+    p.partials = static_cast<float*>(workspace);
+    p.ml = reinterpret_cast<float2*>(p.partials + (size_t)units * a.g.hkv * p.splits * kUnitRows * kHeadDim);
+    p.stall_cycles = test_stall_cycles();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2, 1>(p, map, units, s) : launch<__half, 3, 2>(p, map, units, s);
+}
+
+}  // namespace tq

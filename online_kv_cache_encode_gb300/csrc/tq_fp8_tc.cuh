@@ -1,0 +1,70 @@
+// Tensor-core and TMA building blocks of the 8-bit cache's attention kernels.
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "tq_fp8.cuh"
+#include "tq_tcgen05.cuh"
+
+namespace tq {
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// kind::f8f6f4, e4m3 x e4m3 -> fp32, M = 128; bits 15 and 16 read A and B MN-major
+__device__ constexpr uint32_t idesc_f8(int n, bool mn) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24) | (mn ? (3u << 15) : 0u);
+}
+// Rows of 128 bytes in the 128-byte swizzle, 8-row groups `sbo` bytes apart: K-major as they are, or read MN-major,
+// where 128 e4m3 values fill the one atom along M (its leading offset is not used).
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t sbo) { return tc::smem_desc_sw128(saddr, sbo); }
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar)
+        : "memory");
+}
+// Whether the phase of the given parity is over; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ float redux_max(float x) {  // NaN is ignored
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two 16-bit elements of a word as floats, and back (nearest, ties to even).
+template <typename T>
+__device__ __forceinline__ float2 two_floats(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_two(float lo, float hi) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace tq

@@ -85,13 +85,13 @@ def stored(pool, scales, row, length):
     return x[:, 0, :length], x[:, 1, :length]
 
 
-def attend(q, k, v, limits, sm_scale, keep=None):
+def attend(q, k, v, limits, sm_scale, keep=None, floor=1 / 32):
     """(out, spread, sharp) for q [n, hq, D] over k, v [hkv, L, D]: row i sees tokens t < limits[i] (and keep[t]).
 
     out = sum_t w_t v_t; spread = sum_t w_t |v_t|, what a relative error of the weights is multiplied with; sharp
-    [n, hq] = max_t sum_j (|q_j| + 2^-5 max|q|) |k_tj| sm_scale over the tokens seen, what relative rounding in a
-    score is multiplied with: the products' own, and 2^-21 of the row's largest element where an element far below
-    it is held in fewer bits.  Rows that see nothing are zero."""
+    [n, hq] = max_t sum_j (|q_j| + floor max|q|) |k_tj| sm_scale over the tokens seen, what 2^-16, the relative
+    rounding in a score, is multiplied with: the products' own, and 2^-16 floor of the row's largest element for
+    elements far below it, which are held in fewer bits.  Rows that see nothing are zero."""
     n, hq, _ = q.shape
     hkv, L, _ = k.shape
     x = q.double().view(n, hkv, hq // hkv, D).permute(1, 2, 0, 3)
@@ -104,7 +104,7 @@ def attend(q, k, v, limits, sm_scale, keep=None):
     top = s.amax(-1, keepdim=True) if L else torch.full(s.shape[:-1] + (1,), -math.inf, device=q.device)
     p = torch.exp(s - torch.where(top == -math.inf, torch.zeros_like(top), top))
     w = p / p.sum(-1, keepdim=True).clamp(min=1e-300)
-    sharp = ((x.abs() + x.abs().amax(-1, keepdim=True) / 32) @ k.abs()[:, None].mT * sm_scale).masked_fill(~see, 0.0)
+    sharp = ((x.abs() + x.abs().amax(-1, keepdim=True) * floor) @ k.abs()[:, None].mT * sm_scale).masked_fill(~see, 0.0)
     sharp = sharp.amax(-1) if L else torch.zeros(s.shape[:-1], dtype=torch.float64, device=q.device)
     back = lambda y: y.permute(2, 0, 1, 3).reshape(n, hq, D)  # noqa: E731
     return back(w @ v[:, None]), back(w @ v.abs()[:, None]), sharp.permute(2, 0, 1).reshape(n, hq)
