@@ -26,33 +26,33 @@ constexpr int kRows = 16;  // tokens a warp holds
 
 // Where one warp works: 16 positions of a block.
 struct Place {
-    bool live;       // the unit has tokens and its block lies in the pool
-    int64_t page;    // (block * hkv + head) * 2 + side
+    bool live;       // the unit has tokens there
+    int blk;         // the block's id, not checked yet (-1: past the block table)
     int64_t row0;    // packed row of the warp's first token (may lie before the sequence's first)
     int first;       // offset of the warp's 16 tokens in the block
     int lo, hi;      // offsets in the block of the new tokens: lo <= t < hi
     int head, side;
 };
 
-// Work item `w` (16 tokens) of the launch; WPB = warps per block of tokens.
+// Work item `w` (16 tokens) of the launch; 2^wpb_shift warps per block of tokens.
 __device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch& b, int64_t w, int wpb_shift,
                                             int32_t* status) {
     Place p;
     const int64_t item = w >> wpb_shift;
     p.first = (int)(w & ((1 << wpb_shift) - 1)) * kRows;
     p.side = (int)(item & 1);
-    const int64_t uh = item >> 1;
-    const int64_t u = uh / g.hkv;
-    p.head = (int)(uh - u * g.hkv);
+    const uint32_t uh = (uint32_t)(item >> 1);  // the host keeps the grid, and so this, below 2^31
+    const uint32_t u = uh / (uint32_t)g.hkv;
+    p.head = (int)(uh - u * (uint32_t)g.hkv);
     p.live = false;
-    p.page = 0;
+    p.blk = -1;
     p.row0 = 0;
     p.lo = p.hi = 0;
     if (u >= fp8_units(b.num_tokens, b.batch, g.bs_shift)) return p;
     const int s = fp8_seq_of_unit(b.cu, b.batch, b.num_tokens, u, g.bs_shift);
     const int c0 = fp8_clamp_cu(b.cu, s, b.num_tokens), c1 = fp8_clamp_cu(b.cu, s + 1, b.num_tokens);
     const int n = c1 - c0, start = __ldg(b.start + s);
-    const int64_t j = u - ((int64_t)(c0 >> g.bs_shift) + 2 * (int64_t)s);
+    const int64_t j = (int64_t)u - ((int64_t)(c0 >> g.bs_shift) + 2 * (int64_t)s);
     if (n <= 0 || j < 0) return p;
     if (start < 0) {
         if (j == 0 && (threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
@@ -61,24 +61,36 @@ __device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch
     const int64_t blk_i = (start >> g.bs_shift) + j;  // the block of the sequence
     const int64_t pos0 = blk_i << g.bs_shift;
     if (pos0 >= (int64_t)start + n) return p;
-    const int blk = blk_i < b.max_blocks ? __ldg(b.block_table + (int64_t)s * b.max_blocks + blk_i) : -1;
-    if (blk < 0 || blk >= g.num_blocks) {
-        if ((threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
-        return p;
-    }
+    if (blk_i < b.max_blocks) p.blk = __ldg(b.block_table + (int64_t)s * b.max_blocks + blk_i);
     p.live = true;
-    p.page = ((int64_t)blk * g.hkv + p.head) * 2 + p.side;
     p.row0 = (int64_t)c0 + (pos0 - start) + p.first;
     p.lo = start > pos0 ? (int)(start - pos0) : 0;
     p.hi = (int)min((int64_t)g.bs, (int64_t)start + n - pos0);
     return p;
 }
+// Whether the place's block lies in the pool (else it is flagged); its page is (blk * hkv + head) * 2 + side.
+__device__ __forceinline__ bool page_of(const Fp8Geometry& g, const Place& p, int32_t* status, int64_t& page) {
+    if (p.blk < 0 || p.blk >= g.num_blocks) {
+        if (p.live && (threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
+        return false;
+    }
+    page = ((int64_t)p.blk * g.hkv + p.head) * 2 + p.side;
+    return true;
+}
 
+// A 16-byte piece of a row: V elements.  top() is the largest magnitude as an
+// integer (magnitudes order as their bits do, infinities and NaN above all).
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
-    static constexpr int V = 4;  // elements of a 16-byte piece
+    static constexpr int V = 4;
+    static constexpr uint32_t kInf = 0x7F800000u;
+    static __device__ __forceinline__ uint32_t top(const uint4& r, uint32_t m) {
+        return max(max(m, max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu)), max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
+    }
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return m; }
+    static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m); }
     static __device__ __forceinline__ void get(const uint4& r, float (&x)[4]) {
         x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
     }
@@ -86,9 +98,19 @@ struct Elem<float> {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
 };
-template <>
-struct Elem<__nv_bfloat16> {
+// Two 16-bit elements in a word: magnitudes and maxima two at a time.
+struct Elem16 {
     static constexpr int V = 8;
+    static __device__ __forceinline__ uint32_t top(const uint4& r, uint32_t m) {
+        const uint32_t a = __vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), b = __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu);
+        return __vmaxu2(m, __vmaxu2(a, b));
+    }
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+};
+template <>
+struct Elem<__nv_bfloat16> : Elem16 {
+    static constexpr uint32_t kInf = 0x7F80u;
+    static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m << 16); }
     static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -108,8 +130,9 @@ struct Elem<__nv_bfloat16> {
     }
 };
 template <>
-struct Elem<__half> {
-    static constexpr int V = 8;
+struct Elem<__half> : Elem16 {
+    static constexpr uint32_t kInf = 0x7C00u;
+    static __device__ __forceinline__ float value(uint32_t m) { return __half2float(__ushort_as_half((unsigned short)m)); }
     static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -138,62 +161,68 @@ template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) fp8_write_kernel(const Fp8WriteArgs a, int wpb_shift) {
     using E = Elem<T>;
     constexpr int V = E::V, LPR = kHeadDim / V, RPI = 32 / LPR, IT = kRows / RPI;
-    __shared__ float tops[kWarps];
+    __shared__ uint32_t tops[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
     const Place p = find_place(a.g, a.b, (int64_t)blockIdx.x * kWarps + warp, wpb_shift, a.status);
     const int sub = lane / LPR, col = (lane % LPR) * V;
-    const T* src = static_cast<const T*>(p.side ? a.V : a.K) + p.row0 * (p.side ? a.v_token : a.k_token) +
-                   p.head * (p.side ? a.v_head : a.k_head) + col;
     const int64_t step = p.side ? a.v_token : a.k_token;
+    const T* src = static_cast<const T*>(p.side ? a.V : a.K) + p.row0 * step + p.head * (p.side ? a.v_head : a.k_head) + col;
+    // the rows are on their way before the block's id is looked at
     uint4 raw[IT];
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int r = i * RPI + sub, t = p.first + r;
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (p.live && t >= p.lo && t < p.hi) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + r * step));
+        if (t >= p.lo && t < p.hi) raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + r * step));
     }
+    int64_t page = 0;
+    const bool there = page_of(a.g, p, a.status, page);
     // the block's scale as earlier tokens left it
-    const int e_old = p.live && p.lo > 0 ? fp8_exp_of(a.g.scales[p.page]) : kFp8MinExp;
-    float top = 0.f;
-    bool odd = false;  // an inf or a NaN among the new rows
+    const int e_old = there && p.lo > 0 ? fp8_exp_of(a.g.scales[page]) : kFp8MinExp;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        float x[V];
-        E::get(raw[i], x);
+    for (int i = 0; i < IT; ++i) top = E::top(raw[i], top);
+    top = __reduce_max_sync(0xFFFFFFFFu, E::join(top));
+    const bool odd = top >= E::kInf;  // an inf or a NaN among the new rows: the maximum of the others
+    if (odd) {
+        float best = 0.f;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const bool f = finite(x[k]);
-            odd |= !f;
-            top = fmaxf(top, f ? fabsf(x[k]) : 0.f);
+        for (int i = 0; i < IT; ++i) {
+            float x[V];
+            E::get(raw[i], x);
+#pragma unroll
+            for (int k = 0; k < V; ++k) best = fmaxf(best, finite(x[k]) ? fabsf(x[k]) : 0.f);
         }
+        T b = (T)best;  // exact: one of the elements
+        if constexpr (V == 4) top = __float_as_uint(best);
+        else top = *reinterpret_cast<const unsigned short*>(&b);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (lane == 0) flag(a.status, TQ_FLAG_NONFINITE);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) flag(a.status, TQ_FLAG_NONFINITE);
     if (wpb_shift) {  // the block's warps are neighbours of one CTA
         if (lane == 0) tops[warp] = top;
         __syncthreads();
-        for (int w = 0; w < 1 << wpb_shift; ++w) top = fmaxf(top, tops[(warp >> wpb_shift << wpb_shift) + w]);
+        for (int w = 0; w < 1 << wpb_shift; ++w) top = max(top, tops[(warp >> wpb_shift << wpb_shift) + w]);
     }
-    if (!p.live) return;
-    const int e = max(fp8_exponent(top), e_old);
-    if (p.first == 0 && lane == 0) a.g.scales[p.page] = fp8_pow2(e);
+    if (!there) return;
+    const int e = max(fp8_exponent(E::value(top)), e_old);
+    if (p.first == 0 && lane == 0) a.g.scales[page] = fp8_pow2(e);
     const float inv = fp8_pow2(-e);
-    uint8_t* dst = a.g.pool + p.page * ((int64_t)a.g.bs * kHeadDim) + (int64_t)p.first * kHeadDim + col;
+    uint8_t* dst = a.g.pool + page * ((int64_t)a.g.bs * kHeadDim) + (int64_t)p.first * kHeadDim + col;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int r = i * RPI + sub, t = p.first + r;
         float x[V];
         E::get(raw[i], x);
+        if (odd) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] = x[k] != x[k] ? 0.f : x[k];  // NaN is stored as 0
+        }
         uint32_t w[V / 4];
 #pragma unroll
-        for (int k = 0; k < V; k += 4) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[k + m] = x[k + m] != x[k + m] ? 0.f : x[k + m] * inv;  // NaN is stored as 0
-            w[k / 4] = fp8_cvt2(x[k], x[k + 1]) | (fp8_cvt2(x[k + 2], x[k + 3]) << 16);
-        }
+        for (int k = 0; k < V; k += 4) w[k / 4] = fp8_cvt2(x[k] * inv, x[k + 1] * inv) | (fp8_cvt2(x[k + 2] * inv, x[k + 3] * inv) << 16);
         if (t >= p.lo && t < p.hi) {
             if constexpr (V == 8) *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(w[0], w[V / 4 - 1]);
             else *reinterpret_cast<uint32_t*>(dst + r * kHeadDim) = w[0];
@@ -202,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_write_kernel(const Fp8WriteAr
     if (p.lo > p.first && e > e_old) {  // earlier rows move to the larger scale
         const float m = fp8_pow2(max(e_old - e, -100));
         for (int r = 0; r < min(p.lo - p.first, kRows); ++r) {
-            uint32_t* c = reinterpret_cast<uint32_t*>(a.g.pool + p.page * ((int64_t)a.g.bs * kHeadDim) +
+            uint32_t* c = reinterpret_cast<uint32_t*>(a.g.pool + page * ((int64_t)a.g.bs * kHeadDim) +
                                                       (int64_t)(p.first + r) * kHeadDim) + lane;
             const uint32_t v = *c;
             const float2 x = fp8_to_float2(v & 0xFFFFu), y = fp8_to_float2(v >> 16);
@@ -219,10 +248,11 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_read_kernel(const Fp8ReadArgs
     grid_dependency_wait();
     grid_launch_dependents();
     const Place p = find_place(a.g, a.b, (int64_t)blockIdx.x * kWarps + warp, wpb_shift, a.status);
-    if (!p.live) return;
+    int64_t page = 0;
+    if (!page_of(a.g, p, a.status, page)) return;
     const int sub = lane / LPR, col = (lane % LPR) * V;
-    const float s = __ldg(a.g.scales + p.page);
-    const uint8_t* src = a.g.pool + p.page * ((int64_t)a.g.bs * kHeadDim) + (int64_t)p.first * kHeadDim + col;
+    const float s = __ldg(a.g.scales + page);
+    const uint8_t* src = a.g.pool + page * ((int64_t)a.g.bs * kHeadDim) + (int64_t)p.first * kHeadDim + col;
     T* dst = static_cast<T*>(p.side ? a.V : a.K) + (p.row0 * a.g.hkv + p.head) * kHeadDim + col;
     const int64_t step = (int64_t)a.g.hkv * kHeadDim;
     uint2 raw[IT];
@@ -250,33 +280,28 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_read_kernel(const Fp8ReadArgs
     }
 }
 
-template <typename Args>
-bool grid_of(const Args& a, int& wpb_shift, int64_t& ctas) {
-    wpb_shift = a.g.bs_shift - 4;
-    const int64_t warps = (fp8_units(a.b.num_tokens, a.b.batch, a.g.bs_shift) * a.g.hkv * 2) << wpb_shift;
-    ctas = (warps + kWarps - 1) / kWarps;
-    return ctas <= 0x7FFFFFFF;
+int64_t grid_of(const Fp8Geometry& g, const Fp8Batch& b) {
+    const int64_t warps = (fp8_units(b.num_tokens, b.batch, g.bs_shift) * g.hkv * 2) << (g.bs_shift - 4);
+    return (warps + kWarps - 1) / kWarps;
 }
 
 }  // namespace
 
+bool fp8_rows_count(const Fp8Geometry& g, const Fp8Batch& b) { return grid_of(g, b) < (1 << 28); }
+
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream) {
-    int shift;
-    int64_t ctas;
-    if (!grid_of(a, shift, ctas)) return (int)cudaErrorInvalidConfiguration;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)ctas), block(kWarps * 32);
+    const int shift = a.g.bs_shift - 4;
+    const dim3 grid((unsigned)grid_of(a.g, a.b)), block(kWarps * 32);
     if (a.dtype == TQ_F32) return (int)launch_programmatic(fp8_write_kernel<float>, grid, block, 0, s, a, shift);
     if (a.dtype == TQ_BF16) return (int)launch_programmatic(fp8_write_kernel<__nv_bfloat16>, grid, block, 0, s, a, shift);
     return (int)launch_programmatic(fp8_write_kernel<__half>, grid, block, 0, s, a, shift);
 }
 
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream) {
-    int shift;
-    int64_t ctas;
-    if (!grid_of(a, shift, ctas)) return (int)cudaErrorInvalidConfiguration;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)ctas), block(kWarps * 32);
+    const int shift = a.g.bs_shift - 4;
+    const dim3 grid((unsigned)grid_of(a.g, a.b)), block(kWarps * 32);
     if (a.dtype == TQ_F32) return (int)launch_programmatic(fp8_read_kernel<float>, grid, block, 0, s, a, shift);
     if (a.dtype == TQ_BF16) return (int)launch_programmatic(fp8_read_kernel<__nv_bfloat16>, grid, block, 0, s, a, shift);
     return (int)launch_programmatic(fp8_read_kernel<__half>, grid, block, 0, s, a, shift);

@@ -65,6 +65,7 @@ struct Fp8AttnArgs {
     int32_t* status;
 };
 
+bool fp8_rows_count(const Fp8Geometry& g, const Fp8Batch& b);  // work items are counted in 32 bits
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
 // The pool as rows of 128 codes: the tensor map whose boxes have `rows` of them.

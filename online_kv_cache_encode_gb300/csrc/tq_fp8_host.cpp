@@ -159,10 +159,11 @@ TQ_API tq_status tq_fp8_write(const tq_fp8_cache* c, const void* K, const void* 
     const int64_t elem = dtype == TQ_F32 ? 4 : 2;
     if (bad_rows(K, k_token_stride, k_head_stride, elem) || bad_rows(V, v_token_stride, v_head_stride, elem))
         return fail(TQ_ERR_INVALID_ARG, "the rows of K and V must be 16-byte aligned");
-    if ((st = check_device(c)) != TQ_OK) return st;
     Fp8WriteArgs a{};
     a.g = c->g;
     a.b = make_batch(num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    if (!fp8_rows_count(a.g, a.b)) return fail(TQ_ERR_UNSUPPORTED, "more rows than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
     a.K = K;
     a.V = V;
     a.dtype = (int)dtype;
@@ -183,10 +184,11 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* c, void* K, void* V, tq_dtype d
     if (!known(dtype)) return fail(TQ_ERR_INVALID_ARG, "bad dtype");
     if (!K || !V) return fail(TQ_ERR_INVALID_ARG, "K and V must be non-NULL");
     if (misaligned(K, 16) || misaligned(V, 16)) return fail(TQ_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
-    if ((st = check_device(c)) != TQ_OK) return st;
     Fp8ReadArgs a{};
     a.g = c->g;
     a.b = make_batch(num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    if (!fp8_rows_count(a.g, a.b)) return fail(TQ_ERR_UNSUPPORTED, "more rows than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
     a.K = K;
     a.V = V;
     a.dtype = (int)dtype;

@@ -67,6 +67,7 @@ def test_write(tq, cache):
               dict(ks=(516, 128)), dict(vs=(512, 132)), dict(vs=(512, -8)), dict(dt=0, ks=(514, 128))):
         assert call(**k) == tq.TQ_ERR_INVALID_ARG, k
     assert tq.lib().tq_last_error()
+    assert call(r=ragged(B=(1 << 31) - 1)) == tq.TQ_ERR_UNSUPPORTED
     assert call(r=ragged(T=0, cu=0)) == tq.TQ_OK and call(r=ragged(B=0, cu=0)) == tq.TQ_OK
 
 
@@ -78,6 +79,7 @@ def test_read(tq, cache):
         assert call(r=r) == tq.TQ_ERR_INVALID_ARG, r
     for k in (dict(h=None), dict(K=0), dict(V=0), dict(K=A + 8), dict(dt=-1)):
         assert call(**k) == tq.TQ_ERR_INVALID_ARG, k
+    assert call(r=ragged(B=(1 << 31) - 1)) == tq.TQ_ERR_UNSUPPORTED
     assert call(r=ragged(T=0, cu=0)) == tq.TQ_OK
 
 
@@ -112,6 +114,7 @@ def test_prefill(tq, cache):
         assert call(**k) == getattr(tq, "TQ_ERR_" + e), k
     for r in BATCH:
         assert call(r=r) == tq.TQ_ERR_INVALID_ARG, r
+    assert call(r=ragged(B=(1 << 31) - 1), nws=1 << 60) == tq.TQ_ERR_UNSUPPORTED
     assert call(r=ragged(T=0, cu=0)) == tq.TQ_OK
     L = tq.lib()
     assert L.tq_fp8_prefill_workspace_bytes(cache, 0, 1, 4) == 0 and L.tq_fp8_prefill_workspace_bytes(cache, 9, 0, 4) == 0
