@@ -48,24 +48,6 @@ constexpr int kDecWarps = 12;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr float kPScale = 256.f;      // weights are coded as p * 2^8 <= 256
 
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t* r) {
-    if constexpr (C == 4)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-    else if constexpr (C == 8)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(addr) : "memory");
-    else
-        for (int i = 0; i < C; i += 8) tmem_ld<8>(addr + i, r + i);
-}
-template <int C>
-__device__ __forceinline__ void tmem_ready(uint32_t* r) {  // registers are defined from here on
-    tc::wait_ld();
-#pragma unroll
-    for (int i = 0; i < C; i += 4) asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]));
-}
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Sums C values of every lane over the warp; lane l gets the sum of value l % C.

@@ -25,8 +25,8 @@
 //
 // Warps: 0-3 softmax of A, 4-7 of B (thread = row), 8-11 V's conversion, 12
 // TMA, 13 MMA, 14 scales.  Tensor memory: S_A, S_B (their weights overwrite
-// them), O_A, O_B, 128 columns each.  The maximum of a row moves only when a
-// score beats it by more than 8 (log2 units), by a rescale of O in place.
+// them), O_A, O_B, 128 columns each.  O is rescaled in place where a row's
+// reference rises, which hardly happens after the first step.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -43,7 +43,7 @@ constexpr int kUnitRows = 256;
 constexpr int kTok = 128;                    // tokens of a step
 constexpr int kThreads = 512;
 constexpr int kMetaRing = 4;
-constexpr float kLazyRise = 8.f;
+constexpr float kHeadroom = 24.f;
 
 template <int NT>
 struct PreLayout {
@@ -57,7 +57,8 @@ struct PreLayout {
     static constexpr int bars = okm + kMetaRing * 4 + 16 - kMetaRing * 4 % 16;
     static constexpr int nbars = 2 + 2 * KS + 4 + 4 + 6 + 2 * kMetaRing + 1;
     static constexpr int misc = bars + nbars * 8;
-    static constexpr int total = misc + 16;
+    static constexpr int mult = misc + 16;              // [256] rows' score multipliers
+    static constexpr int total = mult + 256 * 4;
     static constexpr int smem = total + 1024;
     static_assert(k % 1024 == 0 && v % 1024 == 0 && vb % 1024 == 0 && meta % 16 == 0 && bars % 8 == 0, "alignment");
     static_assert(smem <= kSmemLimit, "prefill does not fit in shared memory");
@@ -119,6 +120,17 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// Eight columns of tensor memory; 32 bytes of aligned global memory.
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_32(float* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return sb + L::bars + 8 * i; };
     // queries of a tile stored; keys landed, free; codes of values landed, free; operand of values stored, free;
-    // scores, weights, output of a row tile; scales stored, free; one that nothing arrives on
+    // scores, weights and output of a row tile; scales stored, free; one that nothing arrives on
     constexpr int bQ = 0, bK = 2, bKe = bK + L::KS, bV = bKe + L::KS, bVe = bV + 2, bB = bVe + 2, bBe = bB + 2, bS = bBe + 2,
                   bP = bS + 2, bO = bP + 2, bM = bO + 2, bMe = bM + kMetaRing, bNever = bMe + kMetaRing;
     static_assert(bNever + 1 == L::nbars, "barriers");
@@ -148,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             mbar_init(bar(bB + i), 4);
             mbar_init(bar(bBe + i), 1);
             mbar_init(bar(bS + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(bP + i), 4);
             mbar_init(bar(bO + i), 1);
         }
@@ -188,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         return max(1, (int)((end + kTok - 1) / kTok));
     };
     const int nA = steps_of(0), nB = steps_of(1), nt = max(nA, nB);
-    const int s0 = (int)((int64_t)nt * split / A.splits), s1 = (int)((int64_t)nt * (split + 1) / A.splits);
+    // (fewer than 2^25 steps and at most 64 splits)
+    const int s0 = (int)((uint32_t)nt * split / A.splits), s1 = (int)((uint32_t)nt * (split + 1) / A.splits);
     const int cnt = s1 - s0;
     const int cA = min(max(nA - s0, 0), cnt), cB = min(max(nB - s0, 0), cnt);
     const int64_t slot = ((int64_t)unit * g.hkv + h) * A.splits + split;
@@ -210,167 +225,203 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         // no such unit
     } else if (warp < 8) {
         // ================= softmax: thread = query row =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        const int x = warp >> 2;                       // row tile
-        const int r = tid & 127;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        const int x = warp >> 2, quad = warp & 3;      // row tile, lane quarter
+        const int r = quad * 32 + lane;
         const int tok = U.first + x * A.tpt + r / G;   // new token of the sequence
         const bool there = r < A.tpt * G && tok < U.n;
-        const int64_t out_row = (U.row0 + tok) * A.a.hq + (int64_t)h * G + r % G;
         const int steps = x ? cB : cA;
-        const int64_t pos = (int64_t)U.start + tok;    // attends to tokens 0 .. pos
-        const int64_t pos0 = (int64_t)U.start + U.first + x * A.tpt;  // of the tile's first row
-        const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        // the last token that the row sees, and the tile's first row, counted from this split's first token
+        auto relative = [&](int t) {
+            return (int)max((int64_t)-1, min((int64_t)U.start + t - (int64_t)s0 * kTok, (int64_t)cnt * kTok - 1));
+        };
+        const int pos = relative(tok), pos0 = relative(U.first + x * A.tpt);
+        const uint32_t my = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t tS = my + x * 128, tO = my + 256 + x * 128;
+        float* mult_s = reinterpret_cast<float*>(sm + L::mult) + x * 128;
         bool empty = false;
         if (A.stall_cycles > 0 && (split & 1)) {
             empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
             if (empty && r == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
         }
-        float mult = 0.f;
         if (steps > 0) {
-            // the row's query in e4m3 terms
-            uint4 raw_q[16];
-            const T* q = static_cast<const T*>(A.a.q) + (U.row0 + tok) * A.a.q_token + ((int64_t)h * G + r % G) * A.a.q_head;
+            // the tile's queries in e4m3 terms: a warp takes 32 rows, four elements a lane
+            const int first_row = quad * 32;
+            int row_tok = U.first + x * A.tpt + first_row / G, row_g = first_row % G;
+            constexpr int kBatch = 8;
+            uint2 next[kBatch];
+            auto fetch = [&](int r0) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                raw_q[c] = there ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
-            float top = 0.f;
-            bool odd = false;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t w[4] = {raw_q[c].x, raw_q[c].y, raw_q[c].z, raw_q[c].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = two_floats<T>(w[k]);
-                    odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            }
-            const int e = odd ? 0 : fp8_exponent(top);
-            const float inv = fp8_pow2(-e);
-            mult = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
-            const uint32_t dst = sb + L::q + x * NT * 16384 + r * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 16 elements: one 16-byte piece of every term
-                float y[16];
-                const uint32_t w[8] = {raw_q[2 * c].x,     raw_q[2 * c].y,     raw_q[2 * c].z,     raw_q[2 * c].w,
-                                       raw_q[2 * c + 1].x, raw_q[2 * c + 1].y, raw_q[2 * c + 1].z, raw_q[2 * c + 1].w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 f = two_floats<T>(w[k]);
-                    y[2 * k] = f.x * inv;
-                    y[2 * k + 1] = f.y * inv;
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t lo = fp8_cvt2(y[4 * k], y[4 * k + 1]), hi = fp8_cvt2(y[4 * k + 2], y[4 * k + 3]);
-                        o[k] = lo | (hi << 16);
-                        const float2 a = fp8_to_float2(lo), b = fp8_to_float2(hi);
-                        y[4 * k] -= a.x;
-                        y[4 * k + 1] -= a.y;
-                        y[4 * k + 2] -= b.x;
-                        y[4 * k + 3] -= b.y;
+                for (int i = 0; i < kBatch; ++i) {
+                    const bool in = r0 + i < A.tpt * G && row_tok < U.n;
+                    const T* q = static_cast<const T*>(A.a.q) + (U.row0 + row_tok) * A.a.q_token +
+                                 ((int64_t)h * G + row_g) * A.a.q_head + 4 * lane;
+                    next[i] = in ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
+                    if (++row_g == G) {
+                        row_g = 0;
+                        ++row_tok;
                     }
-                    pre_sts128(dst + j * 16384 + ((c ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                }
+            };
+            fetch(first_row);
+#pragma unroll 1
+            for (int r0 = first_row; r0 < first_row + 32; r0 += kBatch) {
+                uint2 raw_q[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) raw_q[i] = next[i];
+                if (r0 + kBatch < first_row + 32) fetch(r0 + kBatch);  // on their way while these are split
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int row = r0 + i;
+                    const float2 a = two_floats<T>(raw_q[i].x), b = two_floats<T>(raw_q[i].y);
+                    float y[4] = {a.x, a.y, b.x, b.y};
+                    const float top = redux_max(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))));
+                    const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(y[0]) < INFINITY && fabsf(y[1]) < INFINITY &&
+                                                               fabsf(y[2]) < INFINITY && fabsf(y[3]) < INFINITY));
+                    const int e = odd ? 0 : fp8_exponent(top);
+                    const float inv = fp8_pow2(-e);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] *= inv;
+                    const uint32_t at = L::q + x * NT * 16384 + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint32_t lo = fp8_cvt2(y[0], y[1]), hi = fp8_cvt2(y[2], y[3]);
+                        *reinterpret_cast<uint32_t*>(sm + at + j * 16384) = lo | (hi << 16);
+                        const float2 c = fp8_to_float2(lo), d = fp8_to_float2(hi);
+                        y[0] -= c.x;
+                        y[1] -= c.y;
+                        y[2] -= d.x;
+                        y[3] -= d.y;
+                    }
+                    // a query that is not finite makes its own row NaN
+                    if (lane == 0) mult_s[row] = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bQ + x));
         }
-        float m = -INFINITY;  // the reference: raised only when a score beats it by more than kLazyRise
-        float2 sum2 = make_float2(0.f, 0.f);
+        __syncwarp();
+        const float mult = steps > 0 ? mult_s[r] : 0.f;  // stored by this warp
+        // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when
+        // a weight exceeds 1, that is when the 128 weights of a step add up to more than 128: bf16 and fp32 keep their
+        // precision at any size, the sum is needed anyway, and no maximum is formed otherwise (which took a fifth of the
+        // step).  The scores are still in tensor memory then, and the step is weighed again.  A row that has seen no
+        // token yet has no reference.
+        float m = there ? -INFINITY : 0.f;
+        uint64_t acc = f2_pack(0.f, 0.f);
         for (int u = 0; u < steps; ++u) {
             const int mi = u % kMetaRing;
             wait(bM + mi, (u / kMetaRing) & 1);
-            const float* ks = reinterpret_cast<const float*>(sm + L::meta + mi * 64);
             const int ok = *reinterpret_cast<const int*>(sm + L::okm + mi * 4);
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[j] = ks[j] * mult;
-                if (f[j] < 1e-37f) f[j] = 1e-37f;  // a masked score of -inf stays one (NaN stays NaN)
-            }
-            const int64_t tile0 = (int64_t)(s0 + u) * kTok;
+            const float* ks = reinterpret_cast<const float*>(sm + L::meta + mi * 64);
+            auto factor = [&](int j) {  // of tokens 16 j .. (a masked score of -inf stays one; NaN stays NaN)
+                const float y = ks[j] * mult;
+                return y < 1e-37f ? 1e-37f : y;
+            };
+            const int limit = pos - u * kTok;  // the row sees tokens 0 .. limit of the tile
+            const bool masked = ok != 0xFF || u * kTok + kTok - 1 > pos0;  // a mask begins here, or a block is missing
             wait(bS + x, u & 1);
             tc::fence_after_sync();
             __syncwarp();
-            uint32_t s[128];
+            constexpr int kLo = NP == 2 ? 64 : 1;
+            auto load = [&](uint32_t (&s)[128]) {
+                __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-            tc::wait_ld();
+                for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+                tc::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::reg_fence(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-            if (ok != 0xFF || tile0 + kTok - 1 > pos0) {  // somebody's mask begins in this tile, or a page is missing
-                const int64_t rest = pos - tile0;
-                const int limit = rest < -1 ? -1 : rest > kTok ? kTok : (int)rest;  // tokens 0 .. limit of the tile
+                for (int c = 0; c < 4; ++c) tc::reg_fence(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+                if (masked) {
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j > limit || !((ok >> (j >> 4)) & 1)) s[j] = 0xFF800000u;
-            }
-            float mx = -INFINITY;
+                    for (int j = 0; j < 128; ++j)
+                        if (j > limit || !((ok >> (j >> 4)) & 1)) s[j] = 0xFF800000u;
+                }
+            };
+            auto raise = [&](const uint32_t (&s)[128]) {
+                float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {  // the scales are positive: maximum first, scale after
-                float y = -INFINITY;
+                for (int j = 0; j < 8; ++j) {  // the scales are positive: maximum first, scale after
+                    float y = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) y = fmaxf(y, __uint_as_float(s[16 * j + k]));
-                mx = fmaxf(mx, y == -INFINITY ? y : y * f[j]);
-            }
-            const bool rise = mx > m + kLazyRise || (m == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xFFFFFFFFu, rise)) {
-                const float fac = rise ? ex2(m - mx) : 1.f;
-                if (rise) m = mx;
-                sum2.x *= fac;
-                sum2.y *= fac;
-                if (u > 0) {
+                    for (int k = 0; k < 16; ++k) y = fmaxf(y, __uint_as_float(s[16 * j + k]));
+                    mx = fmaxf(mx, y == -INFINITY ? y : y * factor(j));
+                }
+                const bool rise = mx > m;
+                const float fac = rise ? ex2(m - (mx + kHeadroom)) : 1.f;
+                if (rise) m = mx + kHeadroom;
+                acc = f2_mul(acc, f2_pack(fac, fac));
+                if (u > 0 && __any_sync(0xFFFFFFFFu, rise)) {
                     wait(bO + x, (u - 1) & 1);  // the output of the step before is complete
                     tc::fence_after_sync();
                     __syncwarp();
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o[16];
-                        tc::ld_32x32b_x16(tO + 16 * c, o);
-                        tc::wait_ld();
+                    for (int c = 0; c < 16; ++c) {
+                        uint32_t o[8];
+                        tmem_ld<8>(tO + 8 * c, o);
+                        tmem_ready<8>(o);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            asm volatile("" : "+r"(o[k]));
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-                        }
-                        tc::st_32x32b_x16(tO + 16 * c, o);
+                        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+                        tmem_st8(tO + 8 * c, o);
                     }
                     tc::wait_st();
                 }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            const uint64_t neg = f2_pack(-ref, -ref);
-            uint64_t acc = f2_pack(sum2.x, sum2.y), acc2 = f2_pack(0.f, 0.f);
+            };
+            // the scores' weights, packed into the first half of s (their remainders into lo), and their sum
+            auto weigh = [&](uint32_t (&s)[128], uint32_t (&lo)[kLo]) {
+                const float ref = m == -INFINITY ? 0.f : m;
+                const uint64_t neg = f2_pack(-ref, -ref);
+                uint64_t part = f2_pack(0.f, 0.f), part2 = part;
+                uint64_t f2;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const int j = 32 * c + k;
-                    const uint64_t fj = f2_pack(f[j >> 4], f[j >> 4]);
+                for (int j = 0; j < 128; j += 2) {
+                    if (j % 16 == 0) {
+                        const float y = factor(j >> 4);
+                        f2 = f2_pack(y, y);
+                    }
                     float a, b;
                     // a masked score is -inf: its product with a positive scale too
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), fj, neg), a, b);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, neg), a, b);
                     a = ex2(a);
                     b = ex2(b);
-                    if (k & 2) acc = f2_add(acc, f2_pack(a, b));
-                    else acc2 = f2_add(acc2, f2_pack(a, b));
-                    hi[k / 2] = pack_bf16(a, b);
+                    if (j & 2) part = f2_add(part, f2_pack(a, b));
+                    else part2 = f2_add(part2, f2_pack(a, b));
+                    s[j / 2] = pack_bf16(a, b);
                     if constexpr (NP == 2)
-                        lo[k / 2] = pack_bf16(a - __uint_as_float(hi[k / 2] << 16), b - __uint_as_float(hi[k / 2] & 0xFFFF0000u));
+                        lo[j / 2] = pack_bf16(a - __uint_as_float(s[j / 2] << 16), b - __uint_as_float(s[j / 2] & 0xFFFF0000u));
                 }
-                tc::st_32x32b_x16(tS + 16 * c, hi);
-                if constexpr (NP == 2) tc::st_32x32b_x16(tS + 64 + 16 * c, lo);
+                return f2_add(part, part2);
+            };
+            auto store = [&](uint32_t (&s)[128], uint32_t (&lo)[kLo]) {
+                __syncwarp();
+                tc::st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
+                tc::st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                if constexpr (NP == 2) {
+                    tc::st_32x32b_x32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(lo));
+                    tc::st_32x32b_x32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(lo + 32));
+                }
+                tc::wait_st();
+            };
+            bool again = __any_sync(0xFFFFFFFFu, m == -INFINITY);
+            if (!again) {
+                uint32_t s[128], lo[kLo];
+                load(s);
+                const uint64_t part = weigh(s, lo);
+                float a, b;
+                f2_unpack(part, a, b);
+                again = __any_sync(0xFFFFFFFFu, a + b > 128.f);
+                if (!again) {
+                    acc = f2_add(acc, part);
+                    store(s, lo);
+                }
             }
-            acc = f2_add(acc, acc2);
-            f2_unpack(acc, sum2.x, sum2.y);
-            tc::wait_st();
+            if (again) {  // the scores are still in tensor memory
+                uint32_t s[128], lo[kLo];
+                load(s);
+                raise(s);
+                acc = f2_add(acc, weigh(s, lo));
+                store(s, lo);
+            }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bP + x));
@@ -380,33 +431,35 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             flag(A.a.status, TQ_FLAG_TIMEOUT);
             empty = true;
         }
-        const float sum = sum2.x + sum2.y;
+        float sum;
+        {
+            float a, b;
+            f2_unpack(acc, a, b);
+            sum = a + b;
+        }
         if (steps > 0) {
             wait(bO + x, (steps - 1) & 1);
             tc::fence_after_sync();
             __syncwarp();
         }
+        const int64_t out_row = (U.row0 + tok) * A.a.hq + (int64_t)h * G + r % G;
         if (A.splits == 1) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             T* out = static_cast<T*>(A.a.out) + out_row * kHeadDim;
             if (steps > 0)
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc::ld_32x32b_x32(tO + 32 * c, o);
-                    tc::wait_ld();
-                    tc::reg_fence(o);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tmem_ld<16>(tO + 16 * c, o);
+                    tmem_ready<16>(o);
                     if (there && !empty)
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
+                        for (int k = 0; k < 16; k += 8) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float a = sum == 0.f ? 0.f : __uint_as_float(o[k + 2 * i]) * inv;
-                                const float b = sum == 0.f ? 0.f : __uint_as_float(o[k + 2 * i + 1]) * inv;
-                                w[i] = pack_two<T>(a, b);
-                            }
-                            *reinterpret_cast<uint4*>(out + 32 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = sum == 0.f ? 0u : pack_two<T>(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + 16 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                 }
         } else {
@@ -415,20 +468,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             A.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : sum);
             if (steps > 0)
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc::ld_32x32b_x32(tO + 32 * c, o);
-                    tc::wait_ld();
-                    tc::reg_fence(o);
-                    if (there && !none)
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<uint4*>(A.partials + at * kHeadDim + 32 * c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                for (int c = 0; c < 16; ++c) {
+                    uint32_t o[8];
+                    tmem_ld<8>(tO + 8 * c, o);
+                    tmem_ready<8>(o);
+                    if (there && !none) st_global_32(A.partials + at * kHeadDim + 8 * c, o);
                 }
         }
     } else if (warp < 12) {
         // ================= V: codes to bf16, times the block's scale =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int cw = warp - 8;
         for (int u = 0; u < cnt; ++u) {
             const int b = u & 1, mi = u % kMetaRing;
@@ -438,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             const int* vs = reinterpret_cast<const int*>(sm + L::meta + mi * 64 + 32);
             const uint32_t src = sb + L::v + b * 16384, dst = sb + L::vb + b * 32768;
             // a warp converts 32 tokens: 8 of them by 4 pieces of 16 codes at a time
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) {
                 const int t = cw * 32 + (i >> 1) * 8 + (lane & 7), c = (i & 1) * 4 + (lane >> 3);
                 const uint4 v4 = lds128(src + t * 128 + ((c ^ (t & 7)) << 4));
@@ -472,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 12) {
             // ================= TMA: lanes 0-7 the blocks' keys, 8-15 their values =================
             const int pages = kTok >> g.bs_shift, pg = lane & 7, side = (lane >> 3) & 1;

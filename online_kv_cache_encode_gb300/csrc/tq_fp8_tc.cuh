@@ -51,6 +51,25 @@ __device__ __forceinline__ float redux_max(float x) {  // NaN is ignored
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
+// C columns of the thread's tensor-memory lane; the registers hold them after tmem_ready.
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t* r) {
+    if constexpr (C == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else if constexpr (C == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr) : "memory");
+    else
+        for (int i = 0; i < C; i += 8) tmem_ld<8>(addr + i, r + i);
+}
+template <int C>
+__device__ __forceinline__ void tmem_ready(uint32_t* r) {  // registers are defined from here on
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < C; i += 4) asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]));
+}
 // Two 16-bit elements of a word as floats, and back (nearest, ties to even).
 template <typename T>
 __device__ __forceinline__ float2 two_floats(uint32_t w) {
