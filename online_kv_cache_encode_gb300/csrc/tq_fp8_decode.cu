@@ -293,33 +293,15 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 float* mult = reinterpret_cast<float*>(sm + L::mult) + qb * GP;
 #pragma unroll
                 for (int r = 0; r < GP; ++r) {
-                    float x[4];
-                    const float2 q01 = two_floats<T>(rawq[r].x), q23 = two_floats<T>(rawq[r].y);
-                    x[0] = q01.x;
-                    x[1] = q01.y;
-                    x[2] = q23.x;
-                    x[3] = q23.y;
-                    const float top = redux_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-                    const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(x[0]) < INFINITY && fabsf(x[1]) < INFINITY &&
-                                                               fabsf(x[2]) < INFINITY && fabsf(x[3]) < INFINITY));
-                    const int e = odd ? 0 : fp8_exponent(top);
-                    const float inv = fp8_pow2(-e);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] *= inv;
+                    Fp8Split<T> split(rawq[r]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         const int c = j * GP + r;
-                        const uint32_t lo = fp8_cvt2(x[0], x[1]), hi = fp8_cvt2(x[2], x[3]);
-                        *reinterpret_cast<uint32_t*>(sm + L::q + qb * L::q_bytes + c * 128 +
-                                                     (((lane >> 2) ^ (c & 7)) << 4) + (lane & 3) * 4) = lo | (hi << 16);
-                        const float2 y = fp8_to_float2(lo), z = fp8_to_float2(hi);
-                        x[0] = (x[0] - y.x) * 16.f;
-                        x[1] = (x[1] - y.y) * 16.f;
-                        x[2] = (x[2] - z.x) * 16.f;
-                        x[3] = (x[3] - z.y) * 16.f;
+                        *reinterpret_cast<uint32_t*>(sm + L::q + qb * L::q_bytes + c * 128 + (((lane >> 2) ^ (c & 7)) << 4) +
+                                                     (lane & 3) * 4) = split.term(0x4C004C00u);  // the terms 1/16 apart
                     }
                     // a query that is not finite makes its own row NaN
-                    if (lane == 0) mult[r] = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
+                    if (lane == 0) mult[r] = split.factor(A.a.sm_scale_log2);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();

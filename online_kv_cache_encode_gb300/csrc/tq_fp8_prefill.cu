@@ -273,28 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int row = r0 + i;
-                    const float2 a = two_floats<T>(raw_q[i].x), b = two_floats<T>(raw_q[i].y);
-                    float y[4] = {a.x, a.y, b.x, b.y};
-                    const float top = redux_max(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))));
-                    const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(y[0]) < INFINITY && fabsf(y[1]) < INFINITY &&
-                                                               fabsf(y[2]) < INFINITY && fabsf(y[3]) < INFINITY));
-                    const int e = odd ? 0 : fp8_exponent(top);
-                    const float inv = fp8_pow2(-e);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] *= inv;
+                    Fp8Split<T> q(raw_q[i]);
                     const uint32_t at = L::q + x * NT * 16384 + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint32_t lo = fp8_cvt2(y[0], y[1]), hi = fp8_cvt2(y[2], y[3]);
-                        *reinterpret_cast<uint32_t*>(sm + at + j * 16384) = lo | (hi << 16);
-                        const float2 c = fp8_to_float2(lo), d = fp8_to_float2(hi);
-                        y[0] -= c.x;
-                        y[1] -= c.y;
-                        y[2] -= d.x;
-                        y[3] -= d.y;
-                    }
-                    // a query that is not finite makes its own row NaN
-                    if (lane == 0) mult_s[row] = odd ? NAN : A.a.sm_scale_log2 * fp8_pow2(e);
+                    for (int j = 0; j < NT; ++j) *reinterpret_cast<uint32_t*>(sm + at + j * 16384) = q.term(0x3C003C00u);
+                    if (lane == 0) mult_s[row] = q.factor(A.a.sm_scale_log2);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -652,30 +635,43 @@ __global__ void __launch_bounds__(256) fp8_prefill_join_kernel(const PreArgs A) 
     const int64_t uh = item / kUnitRows;
     const int h = (int)(uh % A.a.g.hkv), unit = (int)(uh / A.a.g.hkv);
     if (unit >= pre_units(A.a.b.num_tokens, A.a.b.batch, 2 * A.tpt)) return;
+    // the partials first: where they lie does not depend on the sequence (rows that do not exist are read, not used)
+    const int64_t at = uh * A.splits * kUnitRows + r;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    float all = 0.f, mx = -INFINITY;
+    for (int s0 = 0; s0 < A.splits; s0 += 16) {
+        const int n = min(16, A.splits - s0);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n) ml = A.ml[at + (int64_t)(s0 + lane) * kUnitRows];
+        float4 v[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+            v[s] = s < n ? *(reinterpret_cast<const float4*>(A.partials + (at + (int64_t)(s0 + s) * kUnitRows) * kHeadDim) + lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float top = fmaxf(mx, redux_max(ml.x));
+        const float ref = top == -INFINITY ? 0.f : top, fac = ex2(mx - ref);
+        mx = top;
+        all *= fac;
+        o4.x *= fac;
+        o4.y *= fac;
+        o4.z *= fac;
+        o4.w *= fac;
+        const float w = ex2(ml.x - ref);
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            const float ws = __shfl_sync(0xFFFFFFFFu, w, s), sum = __shfl_sync(0xFFFFFFFFu, ml.y, s);
+            if (sum == 0.f) continue;  // nothing there, and nothing stored
+            all = fmaf(sum, ws, all);
+            o4.x = fmaf(v[s].x, ws, o4.x);
+            o4.y = fmaf(v[s].y, ws, o4.y);
+            o4.z = fmaf(v[s].z, ws, o4.z);
+            o4.w = fmaf(v[s].w, ws, o4.w);
+        }
+    }
     const Unit U = find_unit(A.a.b, unit, 2 * A.tpt);
     const int x = r / kRowsPerTile, rr = r % kRowsPerTile, G = A.a.group;
     const int tok = U.first + x * A.tpt + rr / G;
     if (!U.live || rr >= A.tpt * G || tok >= U.n) return;
-    const int64_t at = uh * A.splits * kUnitRows + r;
-    float mx = -INFINITY;
-    for (int s = lane; s < A.splits; s += 32) mx = fmaxf(mx, A.ml[at + (int64_t)s * kUnitRows].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    float all = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < A.splits; ++s) {
-        const float2 ml = A.ml[at + (int64_t)s * kUnitRows];
-        if (ml.y == 0.f) continue;  // nothing there, and nothing stored
-        const float w = ex2(ml.x - ref);
-        const float4 v = *(reinterpret_cast<const float4*>(A.partials + (at + (int64_t)s * kUnitRows) * kHeadDim) + lane);
-        all = fmaf(ml.y, w, all);
-        o4.x = fmaf(v.x, w, o4.x);
-        o4.y = fmaf(v.y, w, o4.y);
-        o4.z = fmaf(v.z, w, o4.z);
-        o4.w = fmaf(v.w, w, o4.w);
-    }
     const float inv = all == 0.f ? 0.f : 1.f / all;
     T* out = static_cast<T*>(A.a.out) + ((U.row0 + tok) * A.a.hq + (int64_t)h * G + rr % G) * kHeadDim;
     *(reinterpret_cast<uint2*>(out) + lane) = make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));

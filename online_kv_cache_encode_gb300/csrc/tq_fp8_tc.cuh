@@ -86,4 +86,46 @@ __device__ __forceinline__ uint32_t pack_two(float lo, float hi) {
     return r;
 }
 
+// A query row of 128 elements, four a lane, in terms of e4m3: x 2^-e = h1 + h2 + .., with e the exponent that puts
+// the row's largest element into (224, 448].  The whole warp holds one row.  The remainders are exact in fp16, whose
+// 11 bits hold what 16-bit inputs have (elements below 2^-24 / 448 of the row's largest vanish).
+template <typename T>
+struct Fp8Split {
+    uint32_t y01, y23;
+    int e;
+    bool odd;  // an element that is not finite
+    __device__ __forceinline__ explicit Fp8Split(const uint2& raw) {
+        constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t m2 = __vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu);
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));  // magnitudes order as their bits
+        odd = top >= (kB ? 0x7F80u : 0x7C00u);
+        e = odd ? 0 : fp8_exponent(two_floats<T>(top).x);
+        const float inv = fp8_pow2(-e);
+        const float2 a = two_floats<T>(raw.x), b = two_floats<T>(raw.y);
+        y01 = pack_two<__half>(a.x * inv, a.y * inv);
+        y23 = pack_two<__half>(b.x * inv, b.y * inv);
+    }
+    // The next term's four codes; what remains is multiplied by `up` (a pair of fp16 powers of two).
+    __device__ __forceinline__ uint32_t term(uint32_t up) {
+        const uint32_t lo = half2_to_fp8(y01), hi = half2_to_fp8(y23);
+        y01 = rest(y01, fp8_to_half2(lo), up);
+        y23 = rest(y23, fp8_to_half2(hi), up);
+        return lo | (hi << 16);
+    }
+    // What a product with the terms is multiplied with; NaN makes the row NaN.
+    __device__ __forceinline__ float factor(float scale) const { return odd ? NAN : scale * fp8_pow2(e); }
+
+  private:
+    static __device__ __forceinline__ uint32_t half2_to_fp8(uint32_t h) {
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t rest(uint32_t x, uint32_t h, uint32_t up) {
+        uint32_t r;
+        asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}\n" : "=r"(r) : "r"(x), "r"(h), "r"(up));
+        return r;
+    }
+};
+
 }  // namespace tq

@@ -311,6 +311,30 @@ def test_one_token_takes_most_weight(tq, dtype, call):
     sink_case(tq, dtype, call, torch.Generator().manual_seed(77))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("step", [3.0, 40.0, -40.0])
+def test_scores_that_rise_and_fall(tq, dtype, step):
+    """Scores whose size changes by many octaves from tile to tile, up and down: every reference has to follow."""
+    gen = torch.Generator().manual_seed(21)
+    n = 1100
+    s = Setup(tq, gen, [n], 1, 16)
+    q = torch.randn(300, 2, D, generator=gen).to(DT[dtype])
+    q[:, 1] = -q[:, 0]                       # one head's rising scores are the other's falling ones
+    q[1:] = q[:1] * (1 + 0.01 * torch.randn(299, 1, 1, generator=gen)).to(DT[dtype])
+    unit = q[0, 0].float() / q[0, 0].float().norm()
+    K, V = (torch.randn(n, 1, D, generator=gen) for _ in range(2))
+    K[:, 0] += unit * step * torch.arange(n)[:, None] / 64
+    p, sc = R.write(s.pool.cpu(), s.scales.cpu(), K, V, [0, n], [0], s.rows)
+    s.pool.copy_(p)
+    s.scales.copy_(sc)
+    q = q.cuda()
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    out = s.cache.prefill(q, i32([0, 300]), i32([n - 300]), s.table)
+    check(out, q, k, v, [n - 300 + i + 1 for i in range(300)], PREFILL)
+    for m in (n, 700, 257):
+        check(s.cache.decode(q[:1], s.table, i32([m])), q[:1], k[:, :m], v[:, :m], [m], DECODE)
+
+
 @pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_large_and_small_scales(tq, call):
     """Blocks of zeros, of values near the type's limits and of tiny ones, in one sequence; queries of any size."""
