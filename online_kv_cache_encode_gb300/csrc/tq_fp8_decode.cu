@@ -163,8 +163,9 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
     };
     auto tiles = [&](int len) { return max(1, (len + kTile - 1) / kTile); };  // an empty sequence has one, all masked
     // totals stay below 2^31 (the host checks the largest possible)
-    int total = 0;
-    for (int b = lane; b < B; b += 32) total += tiles(length(b));
+    const int len0 = lane < B ? length(lane) : 0;  // of the first 32 sequences, read once
+    int total = lane < B ? tiles(len0) : 0;
+    for (int b = lane + 32; b < B; b += 32) total += tiles(length(b));
     total = __reduce_add_sync(0xFFFFFFFFu, total) * HS;
     const int runs = min((int)gridDim.x, total), cta = (int)blockIdx.x;
     const int each = total / runs, more = total - each * runs;  // the first `more` runs have a tile more
@@ -175,7 +176,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
     if (work) {  // the sequence that tile t0 lies in
         int before = 0;
         for (int b0 = 0;; b0 += 32) {
-            const int b = b0 + lane, len = b < B ? length(b) : 0;
+            const int b = b0 + lane, len = b0 == 0 ? len0 : b < B ? length(b) : 0;
             const int n = b < B ? tiles(len) : 0;
             int inc = n;
 #pragma unroll
@@ -582,10 +583,10 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
                     for (int k = 0; k < H; ++k) acc[k] *= fac[k];
             }
-            take_output(u - 1);
             // ---- the item's end ----
             const float part_sum = sum_lanes<GP>(sum);
             if (lane < GP) sums_s[warp * GP + lane] = part_sum;
+            take_output(u - 1);
             soft_barrier();
             float tot[H];
 #pragma unroll
@@ -622,12 +623,13 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 const int c0 = run_of(a0), c1 = run_of(a1 - 1);
                 soft_barrier();
                 if (tid == 0) {
-                    __threadfence();
+                    // releases what the CTA stored before the barrier, acquires what the others did
                     unsigned* c = A.counters + (int64_t)w.b * HS + w.hs;
-                    const bool last = atomicAdd(c, 1u) == (unsigned)(c1 - c0);
+                    unsigned before;
+                    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(c) : "memory");
+                    const bool last = before == (unsigned)(c1 - c0);
                     if (last) *c = 0u;
                     *last_s = last;
-                    __threadfence();
                 }
                 soft_barrier();
                 if (*last_s) {

@@ -248,28 +248,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             // the tile's queries in e4m3 terms: a warp takes 32 rows, four elements a lane
             const int first_row = quad * 32;
             int row_tok = U.first + x * A.tpt + first_row / G, row_g = first_row % G;
+            // all 32 loads are in flight at once (eight at a time, each batch waited out HBM's latency under the other
+            // CTAs' first loads: 5 us of 8); the split then goes through them by shifting, in a loop small enough for
+            // a cold instruction cache
             constexpr int kBatch = 8;
-            uint2 next[kBatch];
-            auto fetch = [&](int r0) {
+            uint2 raw_q[32];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const bool in = r0 + i < A.tpt * G && row_tok < U.n;
-                    const T* q = static_cast<const T*>(A.a.q) + (U.row0 + row_tok) * A.a.q_token +
-                                 ((int64_t)h * G + row_g) * A.a.q_head + 4 * lane;
-                    next[i] = in ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
-                    if (++row_g == G) {
-                        row_g = 0;
-                        ++row_tok;
-                    }
+            for (int i = 0; i < 32; ++i) {
+                const bool in = first_row + i < A.tpt * G && row_tok < U.n;
+                const T* q = static_cast<const T*>(A.a.q) + (U.row0 + row_tok) * A.a.q_token +
+                             ((int64_t)h * G + row_g) * A.a.q_head + 4 * lane;
+                raw_q[i] = in ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
+                if (++row_g == G) {
+                    row_g = 0;
+                    ++row_tok;
                 }
-            };
-            fetch(first_row);
+            }
 #pragma unroll 1
             for (int r0 = first_row; r0 < first_row + 32; r0 += kBatch) {
-                uint2 raw_q[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) raw_q[i] = next[i];
-                if (r0 + kBatch < first_row + 32) fetch(r0 + kBatch);  // on their way while these are split
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int row = r0 + i;
@@ -279,6 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                     for (int j = 0; j < NT; ++j) *reinterpret_cast<uint32_t*>(sm + at + j * 16384) = q.term(0x3C003C00u);
                     if (lane == 0) mult_s[row] = q.factor(A.a.sm_scale_log2);
                 }
+#pragma unroll
+                for (int i = 0; i + kBatch < 32; ++i) raw_q[i] = raw_q[i + kBatch];
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();

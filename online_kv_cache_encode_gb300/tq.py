@@ -426,15 +426,15 @@ class Fp8Cache:
     def _away(self) -> bool:
         return torch._C._cuda_getDevice() != self._dev
 
-    def _int32(self, *tensors) -> bool:
-        dev = self._dev
-        return all(x.dtype is torch.int32 and x.get_device() == dev and x.is_contiguous() for x in tensors)
+    def _int32(self, x) -> bool:
+        return x.dtype is torch.int32 and x.get_device() == self._dev and x.is_contiguous()
 
     def _batch(self, cu_tokens, start, block_table, status):
         """(batch, max_blocks) of a ragged batch's arguments."""
         B, mb = block_table.shape
-        assert self._int32(cu_tokens, start, block_table), "int32, contiguous, on the cache's device"
-        assert cu_tokens.numel() == B + 1 and start.numel() == B
+        assert self._int32(cu_tokens) and cu_tokens.numel() == B + 1, "cu_tokens: int32 [B + 1] on the cache's device"
+        assert self._int32(start) and start.numel() == B, "start: int32 [B] on the cache's device"
+        assert self._int32(block_table), "block_table: int32, contiguous, on the cache's device"
         assert status is None or self._int32(status)
         return B, mb
 
@@ -513,8 +513,9 @@ class Fp8Cache:
                 return self.decode(q, block_table, lens, sm_scale, out, workspace, status)
         B, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
         rows, mb = block_table.shape
-        assert self._int32(block_table, lens), "int32, contiguous, on the cache's device"
-        assert rows == B and lens.numel() == B and (status is None or self._int32(status))
+        assert rows == B and self._int32(block_table), "block_table: int32 [B, max_blocks] on the cache's device"
+        assert self._int32(lens) and lens.numel() == B, "lens: int32 [B] on the cache's device"
+        assert status is None or self._int32(status)
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if workspace is None:
             workspace = self._workspace("decode", (B, hq), stream, lib().tq_fp8_decode_workspace_bytes)
