@@ -442,8 +442,9 @@ TQ_API void tq_fp8_cache_free(tq_fp8_cache* cache);
  * that starts with new rows does not depend on what was there.  An infinity is
  * stored as the largest code of its sign and a NaN as 0, and both set
  * TQ_FLAG_NONFINITE; they do not enter the maximum.  Every block is written by
- * one group of warps: the same bytes on every run.  Two sequences of a call
- * that write into the same block race. */
+ * one group of warps: the same bytes on every run.  Two positions of a call
+ * that lie in the same block and slot, or two sequences that write into the
+ * same block, race. */
 TQ_API tq_status tq_fp8_write(const tq_fp8_cache* cache, const void* K, const void* V, tq_dtype dtype,
                               int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
                               int64_t v_head_stride, int64_t num_tokens, int batch, const int32_t* cu_tokens,
@@ -469,8 +470,13 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* cache, void* K, void* V, tq_dty
  * num_kv_heads, at most 128 times it.  sm_scale: positive and finite.
  * workspace: device, 256-byte aligned, at least
  * tq_fp8_decode_workspace_bytes(...) bytes, zero-filled once before its first
- * use; each call leaves its counters at zero again.  Two calls in flight at
- * once, replays of captured ones among them, must not share a workspace. */
+ * use; each call leaves its counters at zero again, also one that reported
+ * TQ_FLAG_TIMEOUT, and calls of all shapes on one device may follow one another
+ * on a workspace.  Two calls in flight at once, replays of captured ones among
+ * them, must not share a workspace.
+ * Stored values and queries of 2^-90 .. 2^90 keep the precision of the
+ * accumulators (fp32, scaled by up to 2^-24); a query row that holds a NaN or
+ * an infinity gives NaN in its own output row only. */
 TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* cache, int batch, int num_q_heads);
 TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_seq_stride,
                                          int64_t q_head_stride, int batch, int num_q_heads, const int32_t* block_table,
@@ -480,8 +486,10 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* 
 /* Causal attention of the new tokens of a ragged batch, whose keys and values
  * are in the cache already (tq_fp8_write first): the query row of position p
  * attends over positions 0 .. p.  q and out as for the decode call, with rows
- * [num_tokens, num_q_heads, d] packed like K and V; workspace likewise, with
- * tq_fp8_prefill_workspace_bytes(...). */
+ * [num_tokens, num_q_heads, d] packed like K and V; workspace: at least
+ * tq_fp8_prefill_workspace_bytes(...) bytes of any contents, 256-byte aligned,
+ * not shared by two calls in flight at once (a decode call that takes it over
+ * needs it zero-filled again). */
 TQ_API size_t tq_fp8_prefill_workspace_bytes(const tq_fp8_cache* cache, int64_t num_tokens, int batch, int num_q_heads);
 TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype,
                                           int64_t q_token_stride, int64_t q_head_stride, int64_t num_tokens, int batch,

@@ -713,6 +713,11 @@ int launch(const DecArgs& d, const CUtensorMap& map, int grid, cudaStream_t s) {
 // Query heads go in parts of 8 or 16 columns: 8 where they suffice (fewer exponentials per token).
 int part_of(int group) { return group <= 8 ? 8 : 16; }
 
+// The workspace: the partials, whose size does not depend on the call, and the counters behind them, so that calls of
+// all shapes find every counter at zero where an earlier one left it.
+size_t partial_bytes(const Fp8Geometry& g) {
+    return ((size_t)(g.num_sms > 0 ? g.num_sms : 1) * 2 * kPartFloats * sizeof(float) + 255) / 256 * 256;
+}
 size_t counter_bytes(int batch, int hkv, int group) {
     const int gp = part_of(group);
     return ((size_t)batch * hkv * ((group + gp - 1) / gp) * sizeof(unsigned) + 255) / 256 * 256;
@@ -731,7 +736,7 @@ bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_block
 }
 
 size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group) {
-    return counter_bytes(batch, g.hkv, group) + (size_t)(g.num_sms > 0 ? g.num_sms : 1) * 2 * kPartFloats * sizeof(float);
+    return partial_bytes(g) + counter_bytes(batch, g.hkv, group);
 }
 
 int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream) {
@@ -739,8 +744,8 @@ int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* worksp
     d.a = a;
     const int gp = part_of(a.group);
     d.nsub = (a.group + gp - 1) / gp;
-    d.counters = static_cast<unsigned*>(workspace);
-    d.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(a.b.batch, a.g.hkv, a.group));
+    d.partials = static_cast<float*>(workspace);
+    d.counters = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + partial_bytes(a.g));
     d.stall_cycles = test_stall_cycles();
     const int64_t most = most_tiles(a.g, a.b.batch, a.group, a.b.max_blocks);
     const int grid = (int)(most < a.g.num_sms ? most : a.g.num_sms);

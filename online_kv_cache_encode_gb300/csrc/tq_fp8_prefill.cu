@@ -43,6 +43,7 @@ constexpr int kUnitRows = 256;
 constexpr int kTok = 128;                    // tokens of a step
 constexpr int kThreads = 512;
 constexpr int kMetaRing = 4;
+constexpr int kSoftRegs = 176, kOtherRegs = 80;  // of the two softmax warpgroups and the two others, out of 128 each
 constexpr float kHeadroom = 24.f;
 
 template <int NT>
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         // no such unit
     } else if (warp < 8) {
         // ================= softmax: thread = query row =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2, quad = warp & 3;      // row tile, lane quarter
         const int r = quad * 32 + lane;
         const int tok = U.first + x * A.tpt + r / G;   // new token of the sequence
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         }
     } else if (warp < 12) {
         // ================= V: codes to bf16, times the block's scale =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         const int cw = warp - 8;
         for (int u = 0; u < cnt; ++u) {
             const int b = u & 1, mi = u % kMetaRing;
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 12) {
             // ================= TMA: lanes 0-7 the blocks' keys, 8-15 their values =================
             const int pages = kTok >> g.bs_shift, pg = lane & 7, side = (lane >> 3) & 1;
@@ -691,6 +692,13 @@ int launch(const PreArgs& p, const CUtensorMap& map, int64_t units, cudaStream_t
     static int done[64] = {};
     cudaError_t e = ensure_smem_limit(kern, PreLayout<NT>::smem, done);
     if (e != cudaSuccess) return (int)e;
+    // the warpgroups share out the registers that the block is launched with: a build that gave it fewer would wait for
+    // the rest without end
+    static const bool enough = [&] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess && (f.numRegs + 7) / 8 * 8 * 2 >= kSoftRegs + kOtherRegs;
+    }();
+    if (!enough) return (int)cudaErrorInvalidConfiguration;
     e = launch_programmatic(kern, dim3((unsigned)(units * p.a.g.hkv * p.splits)), dim3(kThreads), (size_t)PreLayout<NT>::smem, s, p, map);
     if (e != cudaSuccess || p.splits == 1) return (int)e;
     return (int)launch_programmatic(fp8_prefill_join_kernel<T>, dim3((unsigned)(units * p.a.g.hkv * (kUnitRows / 8))), dim3(256), 0, s, p);

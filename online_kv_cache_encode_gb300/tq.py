@@ -414,6 +414,7 @@ class Fp8Cache:
             _check(lib().tq_fp8_cache_create(_ptr(pool), _ptr(scales), num_blocks, block_size, num_kv_heads, d,
                                              ctypes.byref(self._h)))
         self._ws = {}
+        self._lib = lib()
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -423,20 +424,19 @@ class Fp8Cache:
 
     # The checks below run on every call of a serving loop: each reads an attribute once, and the device is only
     # switched where the current one is another.
-    def _away(self) -> bool:
-        return torch._C._cuda_getDevice() != self._dev
-
-    def _int32(self, x) -> bool:
-        return x.dtype is torch.int32 and x.get_device() == self._dev and x.is_contiguous()
-
-    def _batch(self, cu_tokens, start, block_table, status):
-        """(batch, max_blocks) of a ragged batch's arguments."""
-        B, mb = block_table.shape
-        assert self._int32(cu_tokens) and cu_tokens.numel() == B + 1, "cu_tokens: int32 [B + 1] on the cache's device"
-        assert self._int32(start) and start.numel() == B, "start: int32 [B] on the cache's device"
-        assert self._int32(block_table), "block_table: int32, contiguous, on the cache's device"
-        assert status is None or self._int32(status)
+    def _batch(self, cu, start, table, status):
+        """(batch, max_blocks) of a ragged batch's arguments: int32, contiguous, on the cache's device."""
+        B, mb = table.shape
+        i32, dev = torch.int32, self._dev
+        assert cu.dtype is i32 and start.dtype is i32 and table.dtype is i32
+        assert cu.get_device() == dev and start.get_device() == dev and table.get_device() == dev
+        assert cu.is_contiguous() and start.is_contiguous() and table.is_contiguous()
+        assert cu.numel() == B + 1 and start.numel() == B
+        assert status is None or self._is_status(status)
         return B, mb
+
+    def _is_status(self, x) -> bool:
+        return x.dtype is torch.int32 and x.get_device() == self._dev and x.numel() >= 1
 
     def _rows(self, x, heads):
         """The token and head strides of rows [T, heads, d] (0 where there is one row only)."""
@@ -461,22 +461,24 @@ class Fp8Cache:
     def write(self, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
               block_table: torch.Tensor, status: torch.Tensor | None = None) -> None:
         """Quantise K, V ([T, num_kv_heads, d], f32/bf16/f16, any token and head strides) into the cache."""
-        if self._away():
+        if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.write(K, V, cu_tokens, start, block_table, status)
         B, mb = self._batch(cu_tokens, start, block_table, status)
         ks, vs = self._rows(K, self.hkv), self._rows(V, self.hkv)
         T, dtype = K.shape[0], K.dtype
         assert V.shape[0] == T and V.dtype is dtype
-        _check(lib().tq_fp8_write(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], *ks, *vs, T, B,
-                                  cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
-                                  torch._C._cuda_getCurrentRawStream(self._dev)))
+        st = self._lib.tq_fp8_write(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], *ks, *vs, T, B,
+                                    cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
+                                    torch._C._cuda_getCurrentRawStream(self._dev))
+        if st:
+            _check(st)
 
     def read(self, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
              dtype: torch.dtype = torch.bfloat16, out: tuple | None = None, status: torch.Tensor | None = None):
         """The stored keys and values of a ragged batch of positions: two [num_tokens, num_kv_heads, d] tensors
         (`out`, or new ones).  Rows that belong to no sequence are not written."""
-        if self._away():
+        if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.read(cu_tokens, start, block_table, num_tokens, dtype, out, status)
         B, mb = self._batch(cu_tokens, start, block_table, status)
@@ -488,9 +490,11 @@ class Fp8Cache:
             for x in out:
                 self._rows(x, self.hkv)
                 assert x.shape[0] == num_tokens and x.dtype is dtype and x.is_contiguous()
-        _check(lib().tq_fp8_read(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], num_tokens, B,
-                                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
-                                 torch._C._cuda_getCurrentRawStream(self._dev)))
+        st = self._lib.tq_fp8_read(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], num_tokens, B,
+                                   cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb, _ptr(status),
+                                   torch._C._cuda_getCurrentRawStream(self._dev))
+        if st:
+            _check(st)
         return K, V
 
     def _attend_args(self, q, sm_scale, out):
@@ -508,20 +512,23 @@ class Fp8Cache:
                status: torch.Tensor | None = None) -> torch.Tensor:
         """q: [B, Hq, d] (bf16/f16, any strides of its first two dimensions); lens: int32 [B] -> out [B, Hq, d]
         of q's type.  A workspace is kept for each stream unless one is given."""
-        if self._away():
+        if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.decode(q, block_table, lens, sm_scale, out, workspace, status)
         B, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
         rows, mb = block_table.shape
-        assert rows == B and self._int32(block_table), "block_table: int32 [B, max_blocks] on the cache's device"
-        assert self._int32(lens) and lens.numel() == B, "lens: int32 [B] on the cache's device"
-        assert status is None or self._int32(status)
+        assert rows == B and lens.numel() == B and lens.dtype is torch.int32 and block_table.dtype is torch.int32
+        assert lens.get_device() == self._dev and block_table.get_device() == self._dev
+        assert lens.is_contiguous() and block_table.is_contiguous()
+        assert status is None or self._is_status(status)
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if workspace is None:
-            workspace = self._workspace("decode", (B, hq), stream, lib().tq_fp8_decode_workspace_bytes)
-        _check(lib().tq_fp8_decode_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, B, hq,
-                                             block_table.data_ptr(), mb, lens.data_ptr(), sm_scale, out.data_ptr(),
-                                             workspace.data_ptr(), workspace.nbytes, _ptr(status), stream))
+            workspace = self._workspace("decode", (B, hq), stream, self._lib.tq_fp8_decode_workspace_bytes)
+        st = self._lib.tq_fp8_decode_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, B, hq,
+                                               block_table.data_ptr(), mb, lens.data_ptr(), sm_scale, out.data_ptr(),
+                                               workspace.data_ptr(), workspace.nbytes, _ptr(status), stream)
+        if st:
+            _check(st)
         return out
 
     def prefill(self, q: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor,
@@ -529,16 +536,18 @@ class Fp8Cache:
                 workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
         """Causal attention of a ragged batch's new tokens (q: [T, Hq, d]; their keys and values written before)
         -> out [T, Hq, d] of q's type.  Rows that belong to no sequence are not written."""
-        if self._away():
+        if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.prefill(q, cu_tokens, start, block_table, sm_scale, out, workspace, status)
         B, mb = self._batch(cu_tokens, start, block_table, status)
         T, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if workspace is None:
-            workspace = self._workspace("prefill", (T, B, hq), stream, lib().tq_fp8_prefill_workspace_bytes)
-        _check(lib().tq_fp8_prefill_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, T, B, hq,
-                                              cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb,
-                                              sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                              _ptr(status), stream))
+            workspace = self._workspace("prefill", (T, B, hq), stream, self._lib.tq_fp8_prefill_workspace_bytes)
+        st = self._lib.tq_fp8_prefill_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, T, B, hq,
+                                                cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb,
+                                                sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                                _ptr(status), stream)
+        if st:
+            _check(st)
         return out

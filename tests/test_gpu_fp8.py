@@ -440,6 +440,26 @@ def test_captured_steps(tq):
         ln += 1
 
 
+def test_one_workspace_for_calls_of_all_shapes(tq):
+    """Small and large batches and head counts in turn on the cache's kept workspace, whose counters must be found at
+    zero by each, and on one that the caller passes."""
+    gen = torch.Generator().manual_seed(14)
+    lens = [1500] + [300] * 40
+    s = Setup(tq, gen, lens, 4, 16)
+    s.fill(lens, outliers=False)
+    q = torch.randn(41, 64, D, generator=gen).bfloat16().cuda()
+    own = torch.zeros(s.cache._lib.tq_fp8_decode_workspace_bytes(s.cache._h, 41, 64), dtype=torch.uint8, device="cuda")
+    cases = [(1, 4), (41, 64), (1, 64), (20, 4), (41, 32), (2, 8), (41, 64), (1, 4)]
+    fresh = []
+    for B, hq in cases:
+        ws = torch.zeros_like(own)
+        fresh.append(s.cache.decode(q[:B, :hq], s.table[:B], i32(lens[:B]), workspace=ws))
+    for _ in range(3):
+        for (B, hq), want in zip(cases, fresh):
+            assert torch.equal(s.cache.decode(q[:B, :hq], s.table[:B], i32(lens[:B])), want)
+            assert torch.equal(s.cache.decode(q[:B, :hq], s.table[:B], i32(lens[:B]), workspace=own), want)
+
+
 def test_two_streams_at_once(tq):
     """Decodes and prefills of the same cache issued on two streams without waiting for one another."""
     gen = torch.Generator().manual_seed(11)
@@ -482,3 +502,28 @@ def test_pool_beyond_32_bits(tq):
     check(c.prefill(q, i32([0, 3]), i32([297]), i32(rows)), q, k, v, [298, 299, 300], PREFILL)
     got = c.read(i32([0, 300]), i32([0]), i32(rows), 300, torch.float32)
     assert torch.equal(got[0].double(), k.permute(1, 0, 2)) and torch.equal(got[1].double(), v.permute(1, 0, 2))
+
+
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+def test_wait_timeout_is_flagged_and_leaves_the_workspace_fit(tq, call):
+    """Every other CTA (decode) or split (prefill) gives up a bounded wait: the call is flagged and returns, and the
+    next one on the same workspace is exact."""
+    gen = torch.Generator().manual_seed(15)
+    n = 9000
+    s = Setup(tq, gen, [n], 1, 16)
+    s.fill([n], outliers=False)
+    q = torch.randn(20, 8, D, generator=gen).bfloat16().cuda()
+    run = (lambda st: s.cache.decode(q[:1], s.table, i32([n]), status=st)) if call == "decode" else (
+        lambda st: s.cache.prefill(q, i32([0, 20]), i32([n - 20]), s.table, status=st))
+    st = tq.new_status()
+    want = run(st)
+    assert st.item() == 0
+    tq.set_test_stall(200000)
+    try:
+        run(st)
+        torch.cuda.synchronize()
+    finally:
+        tq.set_test_stall(0)
+    assert st.item() == tq.FLAG_TIMEOUT
+    st = tq.new_status()
+    assert torch.equal(run(st), want) and st.item() == 0
