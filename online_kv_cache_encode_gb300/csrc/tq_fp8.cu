@@ -48,11 +48,10 @@ __device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch
     p.blk = -1;
     p.row0 = 0;
     p.lo = p.hi = 0;
-    if (u >= fp8_units(b.num_tokens, b.batch, g.bs_shift)) return p;
-    const int s = fp8_seq_of_unit(b.cu, b.batch, b.num_tokens, u, g.bs_shift);
-    const int c0 = fp8_clamp_cu(b.cu, s, b.num_tokens), c1 = fp8_clamp_cu(b.cu, s + 1, b.num_tokens);
-    const int n = c1 - c0, start = __ldg(b.start + s);
-    const int64_t j = (int64_t)u - ((int64_t)(c0 >> g.bs_shift) + 2 * (int64_t)s);
+    if (u >= fp8_units(b.num_tokens, b.batch, g.bs, 2)) return p;
+    const Fp8Seq q = fp8_seq_of_unit(b, u, g.bs, 2);
+    const int s = q.b, c0 = q.row0, n = q.n, start = q.start;
+    const int64_t j = (int64_t)u - q.base;
     if (n <= 0 || j < 0) return p;
     if (start < 0) {
         if (j == 0 && (threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_read_kernel(const Fp8ReadArgs
 }
 
 int64_t grid_of(const Fp8Geometry& g, const Fp8Batch& b) {
-    const int64_t warps = (fp8_units(b.num_tokens, b.batch, g.bs_shift) * g.hkv * 2) << (g.bs_shift - 4);
+    const int64_t warps = (fp8_units(b.num_tokens, b.batch, g.bs, 2) * g.hkv * 2) << (g.bs_shift - 4);
     return (warps + kWarps - 1) / kWarps;
 }
 

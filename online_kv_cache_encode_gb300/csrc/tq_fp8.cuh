@@ -41,26 +41,42 @@ __device__ __forceinline__ int fp8_clamp_cu(const int32_t* cu, int i, int64_t nu
 }
 
 // Work units of a ragged batch, without a prefix sum: sequence b owns the unit
-// numbers from base(b) = cu[b] / step + 2 b up to base(b + 1).  That many,
-// n / step + 2 at least for its n tokens, covers the blocks of `step` positions
-// its tokens touch, wherever they start; the rest of its numbers stay idle.
-// Finds the sequence of unit u (the last b with base(b) <= u) by probing 32
-// places at a time; the whole warp calls it.
-__device__ __forceinline__ int fp8_seq_of_unit(const int32_t* cu, int batch, int64_t num_tokens, int64_t u, int shift) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5;
-        const int i = lo + lane * step;
-        const bool in = lane == 0 || (i < hi && (int64_t)(fp8_clamp_cu(cu, i, num_tokens) >> shift) + 2 * (int64_t)i <= u);
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
-        lo += (31 - __clz((int)m)) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
+// numbers from base(b) = cu[b] / step + extra * b up to base(b + 1).  With
+// extra = 1 that is enough for the ceil(n / step) pieces of its n rows counted
+// from its first, with extra = 2 for the blocks of `step` positions that they
+// touch, wherever they start; the rest of its numbers stay idle.
+__host__ __device__ __forceinline__ int64_t fp8_units(int64_t num_tokens, int batch, int step, int extra) {
+    return num_tokens / step + (int64_t)extra * batch;
 }
-__host__ __device__ __forceinline__ int64_t fp8_units(int64_t num_tokens, int batch, int shift) {
-    return (num_tokens >> shift) + 2 * (int64_t)batch;
+
+// The sequence of a unit (the last b with base(b) <= unit), its packed rows and first position.
+struct Fp8Seq {
+    int b, row0, n, start;
+    int64_t base;
+};
+// Probes 32 places at a time; in the last round the lanes hold 32 neighbours, and what else is wanted of the sequence
+// has been read with them: one round trip to memory for up to 32 sequences, two for 1024.  The whole warp calls it.
+__device__ __forceinline__ Fp8Seq fp8_seq_of_unit(const Fp8Batch& t, int64_t unit, int step, int extra) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = t.batch;
+    while (hi - lo > 32) {
+        const int jump = (hi - lo + 31) >> 5, i = lo + lane * jump;
+        const bool in = lane == 0 || (i < hi && fp8_clamp_cu(t.cu, i, t.num_tokens) / step + (int64_t)extra * i <= unit);
+        lo += (31 - __clz((int)__ballot_sync(0xFFFFFFFFu, in))) * jump;
+        hi = min(hi, lo + jump);
+    }
+    const int i = min(lo + lane, t.batch - 1);
+    const int c0 = fp8_clamp_cu(t.cu, i, t.num_tokens), c1 = fp8_clamp_cu(t.cu, i + 1, t.num_tokens), st = __ldg(t.start + i);
+    const int64_t base = c0 / step + (int64_t)extra * i;
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, lane == 0 || (lo + lane < hi && base <= unit));
+    const int l = 31 - __clz((int)in);
+    Fp8Seq s;
+    s.b = lo + l;
+    s.row0 = __shfl_sync(0xFFFFFFFFu, c0, l);
+    s.n = __shfl_sync(0xFFFFFFFFu, c1, l) - s.row0;
+    s.start = __shfl_sync(0xFFFFFFFFu, st, l);
+    s.base = __shfl_sync(0xFFFFFFFFu, base, l);
+    return s;
 }
 
 }  // namespace tq

@@ -286,24 +286,31 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 const int count = min(GP, A.a.group - sub * GP);
                 const T* q = static_cast<const T*>(A.a.q) + w.b * A.a.q_token +
                              ((int64_t)h * A.a.group + sub * GP) * A.a.q_head + 4 * lane;
-                uint2 rawq[GP];
-#pragma unroll
-                for (int r = 0; r < GP; ++r)
-                    rawq[r] = r < count ? __ldg(reinterpret_cast<const uint2*>(q + r * A.a.q_head)) : make_uint2(0, 0);
-                if (use > 0) wait(bQe + qb, (use - 1) & 1);
-                float* mult = reinterpret_cast<float*>(sm + L::mult) + qb * GP;
+                uint32_t rawq[GP][2];
 #pragma unroll
                 for (int r = 0; r < GP; ++r) {
-                    Fp8Split<T> split(rawq[r]);
+                    const uint2 v = r < count ? __ldg(reinterpret_cast<const uint2*>(q + r * A.a.q_head)) : make_uint2(0, 0);
+                    rawq[r][0] = v.x;
+                    rawq[r][1] = v.y;
+                }
+                if (use > 0) wait(bQe + qb, (use - 1) & 1);
+                float* mult = reinterpret_cast<float*>(sm + L::mult) + qb * GP;
+                Fp8Split<T, 32, GP> split(rawq);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t code[GP][1];
+                    split.template term<0x4C004C00u>(code);  // the terms 1/16 apart
+#pragma unroll
+                    for (int r = 0; r < GP; ++r) {
                         const int c = j * GP + r;
                         *reinterpret_cast<uint32_t*>(sm + L::q + qb * L::q_bytes + c * 128 + (((lane >> 2) ^ (c & 7)) << 4) +
-                                                     (lane & 3) * 4) = split.term(0x4C004C00u);  // the terms 1/16 apart
+                                                     (lane & 3) * 4) = code[r][0];
                     }
-                    // a query that is not finite makes its own row NaN
-                    if (lane == 0) mult[r] = split.factor(A.a.sm_scale_log2);
                 }
+                float factors = 0.f;  // a query that is not finite makes its own row NaN
+#pragma unroll
+                for (int r = 0; r < GP; ++r) factors = lane == r ? split.factor(r, A.a.sm_scale_log2) : factors;
+                if (lane < GP) mult[lane] = factors;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bQ + qb));

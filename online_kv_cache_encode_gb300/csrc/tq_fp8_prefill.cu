@@ -43,7 +43,7 @@ constexpr int kUnitRows = 256;
 constexpr int kTok = 128;                    // tokens of a step
 constexpr int kThreads = 512;
 constexpr int kMetaRing = 4;
-constexpr int kSoftRegs = 176, kOtherRegs = 80;  // of the two softmax warpgroups and the two others, out of 128 each
+constexpr int kSoftRegs = 184, kOtherRegs = 72;  // of the two softmax warpgroups and the two others, out of 128 each
 constexpr float kHeadroom = 24.f;
 
 template <int NT>
@@ -76,23 +76,6 @@ struct PreArgs {
     long long stall_cycles;
 };
 
-// The sequence of unit u, where sequence b owns the numbers from base(b) = cu[b] / step + b on: enough for its
-// ceil(n / step) units wherever it starts.  The whole warp calls it.
-__device__ __forceinline__ int seq_of(const int32_t* cu, int batch, int64_t num_tokens, int u, int step) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int jump = (hi - lo + 31) >> 5, i = lo + lane * jump;
-        const bool in = lane == 0 || (i < hi && fp8_clamp_cu(cu, i, num_tokens) / step + i <= u);
-        lo += (31 - __clz((int)__ballot_sync(0xFFFFFFFFu, in))) * jump;
-        hi = min(hi, lo + jump);
-    }
-    return lo;
-}
-__host__ __device__ __forceinline__ int64_t pre_units(int64_t num_tokens, int batch, int step) {
-    return num_tokens / step + batch;
-}
-
 // A unit: its sequence, packed rows and positions.
 struct Unit {
     int b, n, first;   // sequence, its new tokens, the unit's first among them
@@ -102,14 +85,14 @@ struct Unit {
 };
 __device__ __forceinline__ Unit find_unit(const Fp8Batch& b, int u, int step) {
     Unit x;
-    x.b = seq_of(b.cu, b.batch, b.num_tokens, u, step);
-    const int c0 = fp8_clamp_cu(b.cu, x.b, b.num_tokens), c1 = fp8_clamp_cu(b.cu, x.b + 1, b.num_tokens);
-    x.n = c1 - c0;
-    x.row0 = c0;
-    const int64_t first = ((int64_t)u - (c0 / step + x.b)) * step;
+    const Fp8Seq s = fp8_seq_of_unit(b, u, step, 1);
+    x.b = s.b;
+    x.n = s.n;
+    x.row0 = s.row0;
+    const int64_t first = ((int64_t)u - s.base) * step;
     x.live = first >= 0 && first < x.n;
     x.first = x.live ? (int)first : 0;
-    x.start = __ldg(b.start + x.b);
+    x.start = s.start;
     return x;
 }
 
@@ -207,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
     const int s0 = (int)((uint32_t)nt * split / A.splits), s1 = (int)((uint32_t)nt * (split + 1) / A.splits);
     const int cnt = s1 - s0;
     const int cA = min(max(nA - s0, 0), cnt), cB = min(max(nB - s0, 0), cnt);
-    const int64_t slot = ((int64_t)unit * g.hkv + h) * A.splits + split;
 
     bool bad = false;
     auto wait = [&](int i, uint32_t parity) {
@@ -246,38 +228,54 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             if (empty && r == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
         }
         if (steps > 0) {
-            // the tile's queries in e4m3 terms: a warp takes 32 rows, four elements a lane
-            const int first_row = quad * 32;
+            // the tile's queries in e4m3 terms: a warp takes 32 rows, two at a time (half a warp each, 8 elements a lane).
+            // All 16 loads are in flight at once; the split then goes through them by shifting, in a loop small enough
+            // for a cold instruction cache.
+            const int sub = lane >> 4, col = lane & 15, first_row = quad * 32 + sub;
             int row_tok = U.first + x * A.tpt + first_row / G, row_g = first_row % G;
-            // all 32 loads are in flight at once (eight at a time, each batch waited out HBM's latency under the other
-            // CTAs' first loads: 5 us of 8); the split then goes through them by shifting, in a loop small enough for
-            // a cold instruction cache
-            constexpr int kBatch = 8;
-            uint2 raw_q[32];
+            constexpr int kBatch = 4;
+            uint4 raw_q[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const bool in = first_row + i < A.tpt * G && row_tok < U.n;
+            for (int i = 0; i < 16; ++i) {
+                const bool in = first_row + 2 * i < A.tpt * G && row_tok < U.n;
                 const T* q = static_cast<const T*>(A.a.q) + (U.row0 + row_tok) * A.a.q_token +
-                             ((int64_t)h * G + row_g) * A.a.q_head + 4 * lane;
-                raw_q[i] = in ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
-                if (++row_g == G) {
-                    row_g = 0;
-                    ++row_tok;
-                }
+                             ((int64_t)h * G + row_g) * A.a.q_head + 8 * col;
+                raw_q[i] = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (++row_g == G) {
+                        row_g = 0;
+                        ++row_tok;
+                    }
             }
 #pragma unroll 1
-            for (int r0 = first_row; r0 < first_row + 32; r0 += kBatch) {
+            for (int r0 = first_row; r0 < quad * 32 + 32; r0 += 2 * kBatch) {
+                uint32_t words[kBatch][4];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int row = r0 + i;
-                    Fp8Split<T> q(raw_q[i]);
-                    const uint32_t at = L::q + x * NT * 16384 + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) *reinterpret_cast<uint32_t*>(sm + at + j * 16384) = q.term(0x3C003C00u);
-                    if (lane == 0) mult_s[row] = q.factor(A.a.sm_scale_log2);
+                    words[i][0] = raw_q[i].x;
+                    words[i][1] = raw_q[i].y;
+                    words[i][2] = raw_q[i].z;
+                    words[i][3] = raw_q[i].w;
                 }
+                Fp8Split<T, 16, kBatch> split(words);
 #pragma unroll
-                for (int i = 0; i + kBatch < 32; ++i) raw_q[i] = raw_q[i + kBatch];
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t code[kBatch][2];
+                    split.template term<0>(code);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int row = r0 + 2 * i;
+                        *reinterpret_cast<uint2*>(sm + L::q + (x * NT + j) * 16384 + row * 128 + (((col >> 1) ^ (row & 7)) << 4) +
+                                                  (col & 1) * 8) = make_uint2(code[i][0], code[i][1]);
+                    }
+                }
+                float factors = 0.f;  // a query that is not finite makes its own row NaN
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) factors = col == i ? split.factor(i, A.a.sm_scale_log2) : factors;
+                if (col < kBatch) mult_s[r0 + 2 * col] = factors;
+#pragma unroll
+                for (int i = 0; i + kBatch < 16; ++i) raw_q[i] = raw_q[i + kBatch];
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -285,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         }
         __syncwarp();
         const float mult = steps > 0 ? mult_s[r] : 0.f;  // stored by this warp
+        // the row's place in the output waits there meanwhile: registers are what the loop lacks
+        reinterpret_cast<int*>(mult_s)[r] = there ? (int)(U.row0 + tok) : -1;
         // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when
         // a weight exceeds 1, that is when the 128 weights of a step add up to more than 128: bf16 and fp32 keep their
         // precision at any size, the sum is needed anyway, and no maximum is formed otherwise (which took a fifth of the
@@ -424,17 +424,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             tc::fence_after_sync();
             __syncwarp();
         }
-        const int64_t out_row = (U.row0 + tok) * A.a.hq + (int64_t)h * G + r % G;
+        const int row = reinterpret_cast<const int*>(mult_s)[r];
+        int cta;
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));  // (read again, not held)
+        const int uh2 = cta / A.splits, h2 = uh2 % A.a.g.hkv;
         if (A.splits == 1) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            T* out = static_cast<T*>(A.a.out) + out_row * kHeadDim;
+            T* out = static_cast<T*>(A.a.out) + ((int64_t)row * A.a.hq + (int64_t)h2 * A.a.group + r % A.a.group) * kHeadDim;
             if (steps > 0)
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t o[16];
                     tmem_ld<16>(tO + 16 * c, o);
                     tmem_ready<16>(o);
-                    if (there && !empty)
+                    if (row >= 0 && !empty)
 #pragma unroll
                         for (int k = 0; k < 16; k += 8) {
                             uint32_t w[4];
@@ -445,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                         }
                 }
         } else {
+            const int u_all2 = (int)(gridDim.x / A.splits / A.a.g.hkv);
+            const int64_t slot = ((int64_t)(u_all2 - 1 - uh2 / A.a.g.hkv) * A.a.g.hkv + h2) * A.splits + cta % A.splits;
             const int64_t at = slot * kUnitRows + x * kRowsPerTile + r;
             const bool none = steps == 0 || empty || sum == 0.f;
             A.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : sum);
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                     uint32_t o[8];
                     tmem_ld<8>(tO + 8 * c, o);
                     tmem_ready<8>(o);
-                    if (there && !none) st_global_32(A.partials + at * kHeadDim + 8 * c, o);
+                    if (row >= 0 && !none) st_global_32(A.partials + at * kHeadDim + 8 * c, o);
                 }
         }
     } else if (warp < 12) {
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(256) fp8_prefill_join_kernel(const PreArgs A) 
     const int r = (int)(item % kUnitRows);
     const int64_t uh = item / kUnitRows;
     const int h = (int)(uh % A.a.g.hkv), unit = (int)(uh / A.a.g.hkv);
-    if (unit >= pre_units(A.a.b.num_tokens, A.a.b.batch, 2 * A.tpt)) return;
+    if (unit >= fp8_units(A.a.b.num_tokens, A.a.b.batch, 2 * A.tpt, 1)) return;
     // the partials first: where they lie does not depend on the sequence (rows that do not exist are read, not used)
     const int64_t at = uh * A.splits * kUnitRows + r;
     float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -707,13 +712,13 @@ int launch(const PreArgs& p, const CUtensorMap& map, int64_t units, cudaStream_t
 }  // namespace
 
 bool fp8_prefill_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
-    return pre_units(num_tokens, batch, 2 * tokens_per_tile(group)) * g.hkv * (kUnitRows / 8) < INT_MAX;
+    return fp8_units(num_tokens, batch, 2 * tokens_per_tile(group), 1) * g.hkv * (kUnitRows / 8) < INT_MAX;
 }
 
 size_t fp8_prefill_workspace(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
     const int splits = splits_of(g, num_tokens, batch, group);
     if (splits == 1) return 256;
-    const size_t rows = (size_t)pre_units(num_tokens, batch, 2 * tokens_per_tile(group)) * g.hkv * splits * kUnitRows;
+    const size_t rows = (size_t)fp8_units(num_tokens, batch, 2 * tokens_per_tile(group), 1) * g.hkv * splits * kUnitRows;
     return rows * (kHeadDim * sizeof(float) + sizeof(float2));
 }
 
@@ -722,7 +727,7 @@ int launch_fp8_prefill(const Fp8AttnArgs& a, const CUtensorMap& map, void* works
     p.a = a;
     p.tpt = tokens_per_tile(a.group);
     p.splits = splits_of(a.g, a.b.num_tokens, a.b.batch, a.group);
-    const int64_t units = pre_units(a.b.num_tokens, a.b.batch, 2 * p.tpt);
+    const int64_t units = fp8_units(a.b.num_tokens, a.b.batch, 2 * p.tpt, 1);
     p.partials = static_cast<float*>(workspace);
     p.ml = reinterpret_cast<float2*>(p.partials + (size_t)units * a.g.hkv * p.splits * kUnitRows * kHeadDim);
     p.stall_cycles = test_stall_cycles();

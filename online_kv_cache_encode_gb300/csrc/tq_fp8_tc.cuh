@@ -86,34 +86,62 @@ __device__ __forceinline__ uint32_t pack_two(float lo, float hi) {
     return r;
 }
 
-// A query row of 128 elements, four a lane, in terms of e4m3: x 2^-e = h1 + h2 + .., with e the exponent that puts
-// the row's largest element into (224, 448].  The whole warp holds one row.  The remainders are exact in fp16, whose
-// 11 bits hold what 16-bit inputs have (elements below 2^-24 / 448 of the row's largest vanish).
-template <typename T>
+// Query rows of 128 elements in terms of e4m3: x 2^-e = h1 + h2 + .., with e the exponent that puts the row's largest
+// element into (224, 448].  LANES lanes hold a row, W words of two elements each (the whole warp calls it: 32 lanes a
+// row or 16, two rows at once), and R such rows go through every step together: one at a time its chain of shuffles
+// and conversions took 400 cycles.  The remainders are exact in fp16, whose 11 bits hold what 16-bit inputs have
+// (elements below 2^-24 / 448 of the row's largest vanish).
+template <typename T, int LANES, int R>
 struct Fp8Split {
-    uint32_t y01, y23;
-    int e;
-    bool odd;  // an element that is not finite
-    __device__ __forceinline__ explicit Fp8Split(const uint2& raw) {
-        constexpr bool kB = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t m2 = __vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu);
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));  // magnitudes order as their bits
-        odd = top >= (kB ? 0x7F80u : 0x7C00u);
-        e = odd ? 0 : fp8_exponent(two_floats<T>(top).x);
-        const float inv = fp8_pow2(-e);
-        const float2 a = two_floats<T>(raw.x), b = two_floats<T>(raw.y);
-        y01 = pack_two<__half>(a.x * inv, a.y * inv);
-        y23 = pack_two<__half>(b.x * inv, b.y * inv);
+    static constexpr int W = 64 / LANES;
+    uint32_t y[R][W];
+    int e[R];
+    bool odd[R];  // an element that is not finite
+    __device__ __forceinline__ explicit Fp8Split(const uint32_t (&raw)[R][W]) {
+        uint32_t top[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t m2 = raw[r][0] & 0x7FFF7FFFu;  // magnitudes order as their bits do
+#pragma unroll
+            for (int i = 1; i < W; ++i) m2 = __vmaxu2(m2, raw[r][i] & 0x7FFF7FFFu);
+            top[r] = max(m2 & 0xFFFFu, m2 >> 16);
+        }
+        if constexpr (LANES == 32) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) top[r] = __reduce_max_sync(0xFFFFFFFFu, top[r]);
+        } else {
+#pragma unroll
+            for (int o = LANES / 2; o; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < R; ++r) top[r] = max(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], o));
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            odd[r] = top[r] >= (std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u);
+            e[r] = odd[r] ? 0 : fp8_exponent(two_floats<T>(top[r]).x);
+            const float inv = fp8_pow2(-e[r]);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float2 a = two_floats<T>(raw[r][i]);
+                y[r][i] = pack_two<__half>(a.x * inv, a.y * inv);
+            }
+        }
     }
-    // The next term's four codes; what remains is multiplied by `up` (a pair of fp16 powers of two).
-    __device__ __forceinline__ uint32_t term(uint32_t up) {
-        const uint32_t lo = half2_to_fp8(y01), hi = half2_to_fp8(y23);
-        y01 = rest(y01, fp8_to_half2(lo), up);
-        y23 = rest(y23, fp8_to_half2(hi), up);
-        return lo | (hi << 16);
+    // The next term's codes, four to a word; what remains is multiplied by UP (a pair of fp16 powers of two, or 0: by 1).
+    template <uint32_t UP>
+    __device__ __forceinline__ void term(uint32_t (&w)[R][W / 2]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < W; i += 2) {
+                const uint32_t lo = half2_to_fp8(y[r][i]), hi = half2_to_fp8(y[r][i + 1]);
+                w[r][i / 2] = lo | (hi << 16);
+                y[r][i] = rest<UP>(y[r][i], fp8_to_half2(lo));
+                y[r][i + 1] = rest<UP>(y[r][i + 1], fp8_to_half2(hi));
+            }
     }
-    // What a product with the terms is multiplied with; NaN makes the row NaN.
-    __device__ __forceinline__ float factor(float scale) const { return odd ? NAN : scale * fp8_pow2(e); }
+    // What a product with row r's terms is multiplied with; NaN makes the row NaN.
+    __device__ __forceinline__ float factor(int r, float scale) const { return odd[r] ? NAN : scale * fp8_pow2(e[r]); }
 
   private:
     static __device__ __forceinline__ uint32_t half2_to_fp8(uint32_t h) {
@@ -121,9 +149,11 @@ struct Fp8Split {
         asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
         return r;
     }
-    static __device__ __forceinline__ uint32_t rest(uint32_t x, uint32_t h, uint32_t up) {
+    template <uint32_t UP>
+    static __device__ __forceinline__ uint32_t rest(uint32_t x, uint32_t h) {
         uint32_t r;
-        asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}\n" : "=r"(r) : "r"(x), "r"(h), "r"(up));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(h));
+        if constexpr (UP != 0) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(UP));
         return r;
     }
 };
