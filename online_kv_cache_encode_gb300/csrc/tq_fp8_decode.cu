@@ -645,19 +645,17 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     for (int r = warp; r < count; r += 8) {
                         float mx = -INFINITY, all = 0.f;
                         float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int cb = c0; cb <= c1; cb += 32) {
-                            const int nc = min(32, c1 - cb + 1);
+                        constexpr int kJoin = 24;  // runs at a time: all their loads in flight (a head's 19 to 20 runs at 8 heads)
+                        for (int cb = c0; cb <= c1; cb += kJoin) {
+                            const int nc = min(kJoin, c1 - cb + 1);
                             float2 ml = make_float2(-INFINITY, 0.f);
                             if (lane < nc) ml = __ldcg(reinterpret_cast<const float2*>(of(cb + lane) + 16 * kHeadDim) + r);
-                            float4 v[16];
+                            float4 v[kJoin];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
+                            for (int c = 0; c < kJoin; ++c)
                                 v[c] = c < nc ? __ldcg(reinterpret_cast<const float4*>(of(cb + c) + r * kHeadDim) + lane)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                            float mb = ml.x;
-#pragma unroll
-                            for (int o = 16; o; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
-                            const float mn = fmaxf(mx, mb), ref = mn == -INFINITY ? 0.f : mn, al = ex2(mx - ref);
+                            const float mn = fmaxf(mx, redux_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn, al = ex2(mx - ref);
                             const float wt = ex2(ml.x - ref);
                             float sl = ml.y * wt;
                             mx = mn;
@@ -669,23 +667,12 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                             o4.z *= al;
                             o4.w *= al;
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                if (half) {
-                                    if (nc <= 16) break;
-#pragma unroll
-                                    for (int c = 0; c < 16; ++c)
-                                        v[c] = 16 + c < nc
-                                                   ? __ldcg(reinterpret_cast<const float4*>(of(cb + 16 + c) + r * kHeadDim) + lane)
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                                }
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    const float f = __shfl_sync(0xFFFFFFFFu, wt, 16 * half + c);
-                                    o4.x = fmaf(v[c].x, f, o4.x);
-                                    o4.y = fmaf(v[c].y, f, o4.y);
-                                    o4.z = fmaf(v[c].z, f, o4.z);
-                                    o4.w = fmaf(v[c].w, f, o4.w);
-                                }
+                            for (int c = 0; c < kJoin; ++c) {
+                                const float f = __shfl_sync(0xFFFFFFFFu, wt, c);
+                                o4.x = fmaf(v[c].x, f, o4.x);
+                                o4.y = fmaf(v[c].y, f, o4.y);
+                                o4.z = fmaf(v[c].z, f, o4.z);
+                                o4.w = fmaf(v[c].w, f, o4.w);
                             }
                         }
                         const float inv = all == 0.f ? 0.f : 1048576.f / all;
