@@ -483,8 +483,8 @@ class Fp8Cache:
                 return self.read(cu_tokens, start, block_table, num_tokens, dtype, out, status)
         B, mb = self._batch(cu_tokens, start, block_table, status)
         if out is None:
-            shape, dev = (num_tokens, self.hkv, self.d), self.pool.device
-            K, V = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+            K = torch.empty((num_tokens, self.hkv, self.d), dtype=dtype, device=self.pool.device)
+            V = torch.empty_like(K)
         else:
             K, V = out
             for x in out:
