@@ -10,25 +10,26 @@
 // own (N = NT * GP, padded to 16), so nothing shares a range with anything:
 // 2 terms hold a bf16 query exactly (8 significant bits, to 2^-22 of the row's
 // largest element) and a weight to 2^-8, the rounding of a bf16 output; fp16
-// takes 3 terms, 2^-12.  Each tile's weights are exponentials against the
-// tile's own maximum, so the tokens behind one that dominates a long context
-// keep their relative precision; the tile's output leaves tensor memory and is
-// joined in fp32 registers against the running maximum.  Key scales multiply
-// the scores, value scales the weights (both powers of two).
+// takes 3 terms, 2^-12.  Key scales multiply the scores, value scales the
+// weights (both powers of two).  The weights of a tile are taken against a
+// reference near its own maximum, not the running one, and a tile's output
+// leaves tensor memory and is joined in fp32 registers: the tokens behind one
+// that dominates a long context keep the bits of their weights.
 //
 // What bounds it is the cache's bytes: the tensor work of a tile is about 500
-// cycles and its softmax about as much, against 2850 cycles that HBM needs for
-// its 64 KB on one of 152 SMs.  Hence one CTA per SM, a ring of three 64 KB
-// stages filled by TMA (pages land in the 128-byte swizzle that both readings
-// of a row share), and the flat list of all (sequence, head, tile) cut into
-// equal runs, whatever the lengths are.  An item (sequence, head) that lies in
-// one run is written directly; otherwise each run leaves a partial (max, sum,
+// cycles and its softmax 1000, against 2850 cycles that HBM needs for its 64 KB
+// on one of 152 SMs.  Hence one CTA per SM, a ring of three 64 KB stages filled
+// by TMA (pages land in the 128-byte swizzle that both readings of a row
+// share), and the flat list of all (sequence, head, tile) cut into equal runs,
+// whatever the lengths are.  An item (sequence, head) that lies in one run is
+// written directly; otherwise each run leaves a partial (reference, sum,
 // accumulator) and the last run to arrive joins them in their order, so results
-// do not depend on timing.
+// do not depend on timing.  64 sequences of 1K-16K tokens, 8 KV heads: 188 us,
+// 0.86 of HBM; 32K tokens, 8 heads: 22 us, of which 13 stream (0.75).
 //
 // Warps: 0-7 softmax and accumulation (thread = token of the tile for the
 // scores, = dim for the output, the two warpgroups taking half of the columns
-// each), 8 TMA, 9 MMA, 10 queries, 11 scales.
+// each), 8 and 10 TMA, 9 MMA, 11 queries and scales.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,9 +47,21 @@ constexpr int kSide = kTile * kHeadDim;   // bytes of a tile's keys (or values)
 constexpr int kPagesMax = kTile / 16;
 constexpr int kDecWarps = 12;
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr float kPScale = 256.f;      // weights are coded as p * 2^8 <= 256
+constexpr float kPScale = 256.f;      // weights are coded as p * 2^8 <= 430 (e4m3's largest value is 448)
+constexpr int kWideSpread = 6;        // octaves between a tile's value scales beyond which its weights get their own range
 
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The same, and whether `x` holds in any of the 256 threads: one answer for all, whatever each of them has read.
+__device__ __forceinline__ bool soft_barrier_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
 
 // Sums C values of every lane over the warp; lane l gets the sum of value l % C.
 template <int C>
@@ -83,11 +96,12 @@ struct DecLayout {
     static constexpr int p = kStages * 2 * kSide;
     static constexpr int q = p + 2 * p_bytes;
     static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales [16 each]
-    static constexpr int okm = meta + kStages * 2 * kPagesMax * 4;  // per stage: pages there, largest value exponent
+    static constexpr int okm = meta + kStages * 2 * kPagesMax * 4;  // per stage: pages there (bit 31: wide), largest value exponent
     static constexpr int mult = okm + kStages * 8;          // per query buffer: [GP]
     static constexpr int top = (mult + QB * GP * 4 + 15) / 16 * 16;  // [2][8 warps][GP] maxima
     static constexpr int sums = top + 2 * 8 * GP * 4;       // [8 warps][GP]
-    static constexpr int bars = (sums + 8 * GP * 4 + 7) / 8 * 8;
+    static constexpr int own = sums + 8 * GP * 4;           // [8 warps][2][GP] ranges of wide tiles
+    static constexpr int bars = (own + 8 * 2 * GP * 4 + 7) / 8 * 8;
     static constexpr int nbars = 3 * kStages + 6 + 2 * QB + 1;
     static constexpr int misc = bars + 8 * nbars;           // tmem address, last-arrival word
     static constexpr int total = misc + 16;
@@ -316,9 +330,12 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 if (lane == 0) mbar_arrive(bar(bQ + qb));
             }
             const int e = id >= 0 ? fp8_exp_of(s.y) : -1000;
-            int emax = e;
+            int emax = e, emin = id >= 0 ? e : 1000;
 #pragma unroll
-            for (int o = 8; o; o >>= 1) emax = max(emax, __shfl_xor_sync(0xFFFFFFFFu, emax, o));
+            for (int o = 8; o; o >>= 1) {
+                emax = max(emax, __shfl_xor_sync(0xFFFFFFFFu, emax, o));
+                emin = min(emin, __shfl_xor_sync(0xFFFFFFFFu, emin, o));
+            }
             const unsigned there = __ballot_sync(0xFFFFFFFFu, id >= 0);
             if (ph > 0) wait(bE + st, (ph - 1) & 1);
             float* m = reinterpret_cast<float*>(sm + L::meta) + st * 2 * kPagesMax;
@@ -328,7 +345,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             }
             if (lane == 0) {
                 int* o = reinterpret_cast<int*>(sm + L::okm) + 2 * st;
-                o[0] = (int)there;
+                o[0] = (int)(there | (there && emax - emin > kWideSpread ? 0x80000000u : 0u));
                 o[1] = there ? emax : 0;
             }
             __syncwarp();
@@ -420,6 +437,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         const int dim = quad * 32 + lane;   // output dim
         int* last_s = reinterpret_cast<int*>(sm + L::misc + 8);
         float* sums_s = reinterpret_cast<float*>(sm + L::sums);
+        float* own_s = reinterpret_cast<float*>(sm + L::own) + warp * 2 * GP;
         bool empty = false;  // test hook: this CTA's partials are empty
         if (A.stall_cycles > 0 && (blockIdx.x & 1)) {
             empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
@@ -440,6 +458,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             const int qb = i % L::QB;
             const int n = min(w.nt - w.ti, t1 - t);
             float ref[GP], sum[GP], acc[H], mult[GP], fac[H], vs = 0.f;
+            bool was_wide = false;  // the tile whose output comes next
             float lref[2] = {0.f, 0.f}, lrun[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < GP; ++k) ref[k] = sum[k] = 0.f;
@@ -458,6 +477,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     float x = __uint_as_float(o[(NT - 1) * H + k]);
 #pragma unroll
                     for (int j = NT - 2; j >= 0; --j) x = fmaf(x, 0.0625f, __uint_as_float(o[j * H + k]));
+                    if (was_wide) x *= own_s[(v & 1) * GP + wg * H + k];
                     acc[k] = fmaf(x, vs, acc[k]);
                 }
             };
@@ -502,7 +522,8 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
 #pragma unroll
                     for (int k = 0; k < GP; k += 4)
                         *reinterpret_cast<float4*>(top + warp * GP + k) = make_float4(best[k], best[k + 1], best[k + 2], best[k + 3]);
-                soft_barrier();
+                // (warps whose bounded waits gave up may have read other words, and all have to take the same barriers)
+                const bool wide = soft_barrier_or(okm[0] < 0);
                 if (j == 0 && tid == 0) mbar_arrive(bar(bQe + qb));  // everybody has read the multipliers
                 float2 tile = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
@@ -550,6 +571,29 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                         f2_unpack(f2_mul(p, vr2), x[k], x[k + 1]);
                     }
                 }
+                if (wide) {
+                    // Value scales far apart: a block with a large one, whatever its weights are, must not take the
+                    // range of the others.  The products weight * scale get a range of their own in every column,
+                    // 2^E below the tile's (l + scale exponent has its maximum E above the reference).
+                    const float er = there ? __log2f(vr * (1.f / kPScale)) : 0.f;
+                    float most[GP];
+#pragma unroll
+                    for (int k = 0; k < GP; ++k) most[k] = redux_max(there && vr > 0.f ? l[k] + er : -INFINITY);
+                    if (lane == 0)
+#pragma unroll
+                        for (int k = 0; k < GP; ++k) sums_s[warp * GP + k] = most[k];
+                    soft_barrier();
+#pragma unroll
+                    for (int k = 0; k < GP; ++k) {
+                        float z = -INFINITY;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) z = fmaxf(z, sums_s[y * GP + k]);
+                        const float E = z == -INFINITY ? 0.f : fminf(fmaxf(ceilf(z - ref[k]), -100.f), 0.f);
+                        x[k] *= ex2(-E);
+                        if (lane == k) own_s[(u & 1) * GP + k] = ex2(E);
+                    }
+                    __syncwarp();
+                }
                 // the weights' terms: byte n of the token's 16-column rows
                 uint32_t word[N / 4];
 #pragma unroll
@@ -586,14 +630,15 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 if (lane == 0) mbar_arrive(bar(bP + (u & 1)));
                 if (j > 0) take_output(u - 1);
                 vs = vs_new;
+                was_wide = wide;
                 if (moved)
 #pragma unroll
                     for (int k = 0; k < H; ++k) acc[k] *= fac[k];
             }
             // ---- the item's end ----
             const float part_sum = sum_lanes<GP>(sum);
+            take_output(u - 1);  // (with its wait every warp is past the last tile's use of sums_s)
             if (lane < GP) sums_s[warp * GP + lane] = part_sum;
-            take_output(u - 1);
             soft_barrier();
             float tot[H];
 #pragma unroll

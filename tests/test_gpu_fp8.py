@@ -335,6 +335,39 @@ def test_scores_that_rise_and_fall(tq, dtype, step):
         check(s.cache.decode(q[:1], s.table, i32([m])), q[:1], k[:, :m], v[:, :m], [m], DECODE)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+@pytest.mark.parametrize("octaves", [7, 20, 60])
+def test_large_values_of_negligible_weight(tq, dtype, call, octaves):
+    """Blocks whose values are 2^octaves the others' size but whose weights are 2^-(octaves + 20) and less: they must
+    not cost the others' weights their bits.  In some tiles only, and with a head for which the same blocks weigh in."""
+    gen = torch.Generator().manual_seed(31)
+    n = 900
+    s = Setup(tq, gen, [n], 1, 16)
+    K, V = (torch.randn(n, 1, D, generator=gen) for _ in range(2))
+    q = torch.randn(1, 3, D, generator=gen).to(DT[dtype])
+    u = q[0, 0].float()
+    q[0, 1] = -q[0, 0] / 64
+    big = torch.zeros(n, dtype=torch.bool)
+    big[32:48] = big[256 + 80:256 + 112] = big[896:] = True
+    K[big, 0] -= u * (octaves + 40) * math.log(2) * math.sqrt(D) / float(u @ u)
+    V[big] *= 2.0 ** octaves
+    V[512:528] = 0                               # a block of zeros has the least scale
+    p, sc = R.write(s.pool.cpu(), s.scales.cpu(), K, V, [0, n], [0], s.rows)
+    s.pool.copy_(p)
+    s.scales.copy_(sc)
+    q = q.cuda()
+    out = s.cache.decode(q, s.table, i32([n])) if call == "decode" else s.cache.prefill(q, i32([0, 1]), i32([n - 1]), s.table)
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    floor, most = DECODE if call == "decode" else PREFILL, torch.finfo(out.dtype).max
+    want = R.attend(q, k, v, [n], 1 / math.sqrt(D), None, floor)[0]
+    fits = [h for h in range(3) if want[0, h].abs().max() < most / 2]
+    assert 0 in fits
+    check(out[:, fits], q[:, fits], k, v, [n], floor)
+    over = want.abs() > 2 * most                 # (past fp16: its infinity)
+    assert torch.equal(out[over].double(), want[over].sign() * math.inf)
+
+
 @pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_large_and_small_scales(tq, call):
     """Blocks of zeros, of values near the type's limits and of tiny ones, in one sequence; queries of any size."""
@@ -354,6 +387,46 @@ def test_large_and_small_scales(tq, call):
     q = q.cuda()
     out = s.cache.decode(q, s.table, i32([n])) if call == "decode" else s.cache.prefill(q, i32([0, 1]), i32([n - 1]), s.table)
     check(out, q, *R.stored(s.pool, s.scales, s.rows[0], n), [n], DECODE if call == "decode" else PREFILL)
+
+
+def test_binding_refusals(tq):
+    """What the binding and the library refuse, with nothing launched."""
+    s = Setup(tq, torch.Generator().manual_seed(1), [40], 2, 16)
+    c, cu, st, ln = s.cache, i32([0, 4]), i32([0]), i32([4])
+    K = torch.zeros(4, 2, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 4, D, dtype=torch.bfloat16, device="cuda")
+    before = s.pool.clone()
+    for call in (lambda: c.write(K[:, :1], K[:, :1], cu, st, s.table), lambda: c.write(K, K[:3], cu, st, s.table),
+                 lambda: c.write(K, K.half(), cu, st, s.table), lambda: c.write(K, K, cu.long(), st, s.table),
+                 lambda: c.write(K, K, cu[:1], st, s.table), lambda: c.write(K.cpu(), K.cpu(), cu, st, s.table),
+                 lambda: c.write(K, K, cu, st.cpu(), s.table), lambda: c.write(K, K, cu, st, s.table.t()),
+                 lambda: c.write(K[..., ::2], K[..., ::2], cu, st, s.table),
+                 lambda: c.decode(q, s.table, ln.long()), lambda: c.decode(q, s.table.long(), ln),
+                 lambda: c.decode(q[..., :64], s.table, ln), lambda: c.decode(q, s.table, i32([1, 2])),
+                 lambda: c.decode(q, s.table, ln, out=q.half()), lambda: c.decode(q, s.table, ln, out=q.expand(1, 4, D)[:, :2]),
+                 lambda: c.read(cu, st, s.table, 4, torch.bfloat16, out=(K, K.half())),
+                 lambda: c.prefill(q, cu, st, s.table, status=torch.zeros(1, device="cuda"))):
+        with pytest.raises(AssertionError):
+            call()
+    for call, status in ((lambda: c.decode(q.float(), s.table, ln), tq.TQ_ERR_UNSUPPORTED),
+                         (lambda: c.prefill(q.float(), i32([0, 1]), st, s.table), tq.TQ_ERR_UNSUPPORTED),
+                         (lambda: c.decode(q[:, :3], s.table, ln), tq.TQ_ERR_INVALID_ARG),
+                         (lambda: c.decode(q, s.table, ln, sm_scale=-1.0), tq.TQ_ERR_INVALID_ARG),
+                         (lambda: c.decode(q, s.table, ln, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")),
+                          tq.TQ_ERR_WORKSPACE),
+                         (lambda: c.write(K.view(-1)[4:4 + 3 * 2 * D].view(3, 2, D), K[:3], cu, st, s.table),
+                          tq.TQ_ERR_INVALID_ARG)):
+        with pytest.raises(tq.TQError) as e:
+            call()
+        assert e.value.status == status
+    torch.cuda.synchronize()
+    assert torch.equal(s.pool, before)
+    # nothing to do is not an error
+    none = K[:0]
+    c.write(none, none, i32([0, 0]), st, s.table)
+    assert c.decode(q[:0], s.table[:0], ln[:0]).shape == (0, 4, D)
+    assert c.prefill(q[:0], i32([0, 0]), st, s.table).shape == (0, 4, D)
+    assert c.read(i32([0, 0]), st, s.table, 0)[0].shape == (0, 2, D)
 
 
 @pytest.mark.parametrize("call", ["decode", "prefill"])
