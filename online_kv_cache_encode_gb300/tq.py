@@ -524,6 +524,8 @@ class Fp8Cache:
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if workspace is None:
             workspace = self._workspace("decode", (B, hq), stream, self._lib.tq_fp8_decode_workspace_bytes)
+        else:
+            assert workspace.get_device() == self._dev and workspace.is_contiguous()
         st = self._lib.tq_fp8_decode_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, B, hq,
                                                block_table.data_ptr(), mb, lens.data_ptr(), sm_scale, out.data_ptr(),
                                                workspace.data_ptr(), workspace.nbytes, _ptr(status), stream)
@@ -544,6 +546,8 @@ class Fp8Cache:
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if workspace is None:
             workspace = self._workspace("prefill", (T, B, hq), stream, self._lib.tq_fp8_prefill_workspace_bytes)
+        else:
+            assert workspace.get_device() == self._dev and workspace.is_contiguous()
         st = self._lib.tq_fp8_prefill_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, T, B, hq,
                                                 cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb,
                                                 sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,

@@ -368,6 +368,37 @@ def test_large_values_of_negligible_weight(tq, dtype, call, octaves):
     assert torch.equal(out[over].double(), want[over].sign() * math.inf)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bs", [16, 64])
+def test_runs_of_tiles_with_and_without_far_scales(tq, dtype, bs):
+    """The same blocks read by 300 sequences of other lengths, so that a CTA goes through several tiles whose value
+    scales lie far apart in some and near in others, and through several sequences."""
+    gen = torch.Generator().manual_seed(37)
+    n, B = 1500, 300
+    s = Setup(tq, gen, [n], 1, bs)
+    K, V = (torch.randn(n, 1, D, generator=gen) for _ in range(2))
+    u = torch.randn(D, generator=gen)
+    q = (u * (1 + 0.05 * torch.randn(B, 10, 1, generator=gen))).to(DT[dtype])
+    q[::2, 1:3] = (torch.randn((B + 1) // 2, 2, D, generator=gen)).to(DT[dtype])
+    big = torch.zeros(n, dtype=torch.bool)
+    big[64:128] = big[832:896] = big[1472:] = True
+    K[big, 0] -= u * 40 * math.log(2) * math.sqrt(D) / float(u @ u)
+    V[big] *= 2.0 ** 10
+    V[320:384] *= 2.0 ** -12
+    p, sc = R.write(s.pool.cpu(), s.scales.cpu(), K, V, [0, n], [0], s.rows)
+    s.pool.copy_(p)
+    s.scales.copy_(sc)
+    lens = torch.randint(0, n + 1, (B,), generator=gen).tolist()
+    lens[:4] = [0, 1, n, n]
+    q = q.cuda()
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    table = s.table.repeat(B, 1)
+    for heads in (3, 10):
+        out = s.cache.decode(q[:, :heads], table, i32(lens))
+        assert not out[0].any()
+        check(out[1:], q[1:, :heads], k, v, lens[1:], DECODE)
+
+
 @pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_large_and_small_scales(tq, call):
     """Blocks of zeros, of values near the type's limits and of tiny ones, in one sequence; queries of any size."""
@@ -404,6 +435,8 @@ def test_binding_refusals(tq):
                  lambda: c.decode(q, s.table, ln.long()), lambda: c.decode(q, s.table.long(), ln),
                  lambda: c.decode(q[..., :64], s.table, ln), lambda: c.decode(q, s.table, i32([1, 2])),
                  lambda: c.decode(q, s.table, ln, out=q.half()), lambda: c.decode(q, s.table, ln, out=q.expand(1, 4, D)[:, :2]),
+                 lambda: c.decode(q, s.table, ln, workspace=torch.zeros(1 << 24, dtype=torch.uint8)),
+                 lambda: c.prefill(q, i32([0, 1]), st, s.table, workspace=torch.zeros(1 << 24, dtype=torch.uint8)),
                  lambda: c.read(cu, st, s.table, 4, torch.bfloat16, out=(K, K.half())),
                  lambda: c.prefill(q, cu, st, s.table, status=torch.zeros(1, device="cuda"))):
         with pytest.raises(AssertionError):
@@ -511,6 +544,54 @@ def test_captured_steps(tq):
             check(out[b:b + 1], x[b:b + 1, :hq], *R.stored(s.pool, s.scales, s.rows[b], n[b]), [n[b]], DECODE)
         start += 1
         ln += 1
+
+
+def test_captured_prompt(tq):
+    """A chunk's write, its attention (split over the tokens, so with a workspace) and a read back, captured once and
+    replayed with other rows, positions and lengths, an idle sequence and rows behind the last one among them."""
+    gen = torch.Generator().manual_seed(41)
+    lens, hq, hkv, T = [900, 300], 4, 2, 96
+    s = Setup(tq, gen, lens, hkv, 32)
+    K, V = (torch.randn(T, hkv, D, generator=gen).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(T, hq, D, generator=gen).bfloat16().cuda()
+    cu, st = i32([0, 0, 0]), i32([0, 0])
+    cu_all, zero = i32([0, 900, 1200]), i32([0, 0])
+    prefix = [torch.randn(1200, hkv, D, generator=gen).bfloat16().cuda() for _ in range(2)]
+    out, back = torch.empty_like(q), (torch.empty_like(K), torch.empty_like(V))
+
+    def step():
+        s.cache.write(K, V, cu, st, s.table)
+        s.cache.prefill(q, cu, st, s.table, out=out)
+        s.cache.read(cu, st, s.table, T, out=back)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for cut, start in (([0, 96, 96], [800, 0]), ([0, 40, 90], [13, 250]), ([0, 0, 1], [5, 299]), ([0, 50, 96], [0, 0])):
+        s.cache.write(*prefix, cu_all, zero, s.table)
+        K.copy_(torch.randn(T, hkv, D, generator=gen))
+        V.copy_(torch.randn(T, hkv, D, generator=gen))
+        q.copy_(torch.randn(T, hq, D, generator=gen))
+        cu.copy_(i32(cut))
+        st.copy_(i32(start))
+        for x in (out, *back):
+            x.fill_(7)
+        want = [x.cpu() for x in (s.pool, s.scales)]
+        graph.replay()
+        want = R.write(*want, K.cpu().float(), V.cpu().float(), cut, start, s.rows)
+        assert torch.equal(s.pool.cpu(), want[0])
+        assert torch.equal(s.scales.cpu().view(torch.int32), want[1].view(torch.int32))
+        for b in range(2):
+            a, z = cut[b], cut[b + 1]
+            if z > a:
+                k, v = R.stored(s.pool, s.scales, s.rows[b], start[b] + z - a)
+                check(out[a:z], q[a:z], k, v, [start[b] + i + 1 for i in range(z - a)], PREFILL)
+                for x, y in zip(back, (k, v)):
+                    assert torch.equal(x[a:z], y[:, start[b]:].permute(1, 0, 2).to(torch.bfloat16))
+        for x in (out, *back):
+            assert (x[cut[-1]:] == 7).all()
 
 
 def test_one_workspace_for_calls_of_all_shapes(tq):
