@@ -95,12 +95,12 @@ struct DecLayout {
     static constexpr int q_bytes = N * kHeadDim;
     static constexpr int p = kStages * 2 * kSide;
     static constexpr int q = p + 2 * p_bytes;
-    static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales [16 each]
+    static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales (wide: exponents) [16 each]
     static constexpr int okm = meta + kStages * 2 * kPagesMax * 4;  // per stage: pages there (bit 31: wide), largest value exponent
     static constexpr int mult = okm + kStages * 8;          // per query buffer: [GP]
     static constexpr int top = (mult + QB * GP * 4 + 15) / 16 * 16;  // [2][8 warps][GP] maxima
     static constexpr int sums = top + 2 * 8 * GP * 4;       // [8 warps][GP]
-    static constexpr int own = sums + 8 * GP * 4;           // [8 warps][2][GP] ranges of wide tiles
+    static constexpr int own = sums + 8 * GP * 4;           // [8 warps][2][GP] output factors of wide tiles
     static constexpr int bars = (own + 8 * 2 * GP * 4 + 7) / 8 * 8;
     static constexpr int nbars = 3 * kStages + 6 + 2 * QB + 1;
     static constexpr int misc = bars + 8 * nbars;           // tmem address, last-arrival word
@@ -332,20 +332,21 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             const int e = id >= 0 ? fp8_exp_of(s.y) : -1000;
             int emax = e, emin = id >= 0 ? e : 1000;
 #pragma unroll
-            for (int o = 8; o; o >>= 1) {
+            for (int o = 8; o; o >>= 1) {  // (lanes 0-15 hold the blocks)
                 emax = max(emax, __shfl_xor_sync(0xFFFFFFFFu, emax, o));
                 emin = min(emin, __shfl_xor_sync(0xFFFFFFFFu, emin, o));
             }
             const unsigned there = __ballot_sync(0xFFFFFFFFu, id >= 0);
+            const bool wide = emax - emin > kWideSpread;  // (without blocks emin > emax)
             if (ph > 0) wait(bE + st, (ph - 1) & 1);
             float* m = reinterpret_cast<float*>(sm + L::meta) + st * 2 * kPagesMax;
             if (lane < 16) {
                 m[lane] = s.x;
-                m[16 + lane] = id >= 0 && e - emax > -126 ? fp8_pow2(e - emax) : 0.f;
+                m[16 + lane] = id < 0 ? 0.f : wide ? (float)(e - emax) : fp8_pow2(e - emax);
             }
             if (lane == 0) {
                 int* o = reinterpret_cast<int*>(sm + L::okm) + 2 * st;
-                o[0] = (int)(there | (there && emax - emin > kWideSpread ? 0x80000000u : 0u));
+                o[0] = (int)(there | (wide ? 0x80000000u : 0u));
                 o[1] = there ? emax : 0;
             }
             __syncwarp();
@@ -477,8 +478,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     float x = __uint_as_float(o[(NT - 1) * H + k]);
 #pragma unroll
                     for (int j = NT - 2; j >= 0; --j) x = fmaf(x, 0.0625f, __uint_as_float(o[j * H + k]));
-                    if (was_wide) x *= own_s[(v & 1) * GP + wg * H + k];
-                    acc[k] = fmaf(x, vs, acc[k]);
+                    acc[k] = fmaf(x, was_wide ? own_s[(v & 1) * GP + wg * H + k] : vs, acc[k]);
                 }
             };
             wait(bQ + qb, (i / L::QB) & 1);
@@ -574,23 +574,25 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 if (wide) {
                     // Value scales far apart: a block with a large one, whatever its weights are, must not take the
                     // range of the others.  The products weight * scale get a range of their own in every column,
-                    // 2^E below the tile's (l + scale exponent has its maximum E above the reference).
-                    const float er = there ? __log2f(vr * (1.f / kPScale)) : 0.f;
+                    // 2^E below the tile's (l + scale exponent has its maximum E above the reference), down to where
+                    // the output's factor is a normal number.  The scale's place holds its exponent, for any distance.
+                    const float er = me[16 + pg];
                     float most[GP];
 #pragma unroll
-                    for (int k = 0; k < GP; ++k) most[k] = redux_max(there && vr > 0.f ? l[k] + er : -INFINITY);
+                    for (int k = 0; k < GP; ++k) most[k] = redux_max(there ? l[k] + er : -INFINITY);
                     if (lane == 0)
 #pragma unroll
                         for (int k = 0; k < GP; ++k) sums_s[warp * GP + k] = most[k];
                     soft_barrier();
+                    const float least = (float)(-98 - okm[1]);
 #pragma unroll
                     for (int k = 0; k < GP; ++k) {
                         float z = -INFINITY;
 #pragma unroll
                         for (int y = 0; y < 8; ++y) z = fmaxf(z, sums_s[y * GP + k]);
-                        const float E = z == -INFINITY ? 0.f : fminf(fmaxf(ceilf(z - ref[k]), -100.f), 0.f);
-                        x[k] *= ex2(-E);
-                        if (lane == k) own_s[(u & 1) * GP + k] = ex2(E);
+                        const float E = z == -INFINITY ? 0.f : fminf(fmaxf(ceilf(z - ref[k]), least), 0.f);
+                        x[k] = kPScale * ex2((l[k] - ref[k]) + (er - E));
+                        if (lane == k) own_s[(u & 1) * GP + k] = E == 0.f ? vs_new : fp8_pow2((int)E + okm[1] - 28);
                     }
                     __syncwarp();
                 }
