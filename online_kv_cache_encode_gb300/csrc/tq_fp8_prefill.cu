@@ -104,15 +104,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Eight columns of tensor memory; 32 bytes of aligned global memory.
+// Eight columns of tensor memory.
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void st_global_32(float* p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -428,38 +423,59 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         int cta;
         asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));  // (read again, not held)
         const int uh2 = cta / A.splits, h2 = uh2 % A.a.g.hkv;
+        // A thread has a row of its own in tensor memory; rows of 16-byte pieces leave through shared memory (the place
+        // of the tile's queries, whose last reader is done), so that a store takes two rows and not 32 pieces 4 KB apart
+        // (which cost 4000 cycles of the unit's end).
+        const uint32_t stage = sb + L::q + x * NT * 16384 + quad * 8192;
+        auto leave = [&](char* mine) {  // 256 bytes of every row to `mine` of its thread (null: nowhere)
+            __syncwarp();
+#pragma unroll (NT == 2 ? 4 : 1)
+            for (int i = 0; i < 16; ++i) {
+                const int from = 2 * i + (lane >> 4);
+                const uint64_t to = __shfl_sync(0xFFFFFFFFu, (unsigned long long)mine, from);
+                const uint4 v = lds128(stage + from * 256 + (((lane & 15) ^ (from & 7)) << 4));
+                if (to) *reinterpret_cast<uint4*>(to + 16 * (lane & 15)) = v;
+            }
+            __syncwarp();
+        };
+        auto piece = [&](int i) { return stage + lane * 256 + ((i ^ (lane & 7)) << 4); };
         if (A.splits == 1) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             T* out = static_cast<T*>(A.a.out) + ((int64_t)row * A.a.hq + (int64_t)h2 * A.a.group + r % A.a.group) * kHeadDim;
-            if (steps > 0)
+            if (steps > 0) {
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t o[16];
                     tmem_ld<16>(tO + 16 * c, o);
                     tmem_ready<16>(o);
-                    if (row >= 0 && !empty)
+                    uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 16; k += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = sum == 0.f ? 0u : pack_two<T>(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
-                            *reinterpret_cast<uint4*>(out + 16 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = sum == 0.f ? 0u : pack_two<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                    pre_sts128(piece(2 * c), w[0], w[1], w[2], w[3]);
+                    pre_sts128(piece(2 * c + 1), w[4], w[5], w[6], w[7]);
                 }
+                leave(row >= 0 && !empty ? reinterpret_cast<char*>(out) : nullptr);
+            }
         } else {
             const int u_all2 = (int)(gridDim.x / A.splits / A.a.g.hkv);
             const int64_t slot = ((int64_t)(u_all2 - 1 - uh2 / A.a.g.hkv) * A.a.g.hkv + h2) * A.splits + cta % A.splits;
             const int64_t at = slot * kUnitRows + x * kRowsPerTile + r;
             const bool none = steps == 0 || empty || sum == 0.f;
             A.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : sum);
+            char* part = row >= 0 && !none ? reinterpret_cast<char*>(A.partials + at * kHeadDim) : nullptr;
             if (steps > 0)
 #pragma unroll 1
-                for (int c = 0; c < 16; ++c) {
-                    uint32_t o[8];
-                    tmem_ld<8>(tO + 8 * c, o);
-                    tmem_ready<8>(o);
-                    if (row >= 0 && !none) st_global_32(A.partials + at * kHeadDim + 8 * c, o);
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+                        tmem_ld<16>(tO + 64 * half + 16 * c, o);
+                        tmem_ready<16>(o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) pre_sts128(piece(4 * c + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                    leave(part ? part + 256 * half : nullptr);
                 }
         }
     } else if (warp < 12) {
