@@ -23,8 +23,8 @@
 // tensor cores work on one while the softmax of the other runs, and both use
 // the same K and V.
 //
-// Warps: 0-3 softmax of A, 4-7 of B (thread = row), 8-11 V's conversion, 12
-// TMA, 13 MMA, 14 scales.  Tensor memory: S_A, S_B (their weights overwrite
+// Warps: 0-3 softmax of A, 4-7 of B (thread = row), 8-11 V's conversion (these
+// twelve split the queries first), 12 TMA, 13 MMA, 14 scales.  Tensor memory: S_A, S_B (their weights overwrite
 // them), O_A, O_B, 128 columns each.  O is rescaled in place where a row's
 // reference rises, which hardly happens after the first step.
 #include <cuda.h>
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(bQ + i), 4);
+            mbar_init(bar(bQ + i), 6);
             mbar_init(bar(bV + i), 1);
             mbar_init(bar(bVe + i), 4);
             mbar_init(bar(bB + i), 4);
@@ -199,40 +199,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         return id >= 0 && id < g.num_blocks ? id : -2;
     };
 
-    if (!U.live) {
-        // no such unit
-    } else if (warp < 8) {
-        // ================= softmax: thread = query row =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int x = warp >> 2, quad = warp & 3;      // row tile, lane quarter
-        const int r = quad * 32 + lane;
-        const int tok = U.first + x * A.tpt + r / G;   // new token of the sequence
-        const bool there = r < A.tpt * G && tok < U.n;
-        const int steps = x ? cB : cA;
-        // the last token that the row sees, and the tile's first row, counted from this split's first token
-        auto relative = [&](int t) {
-            return (int)max((int64_t)-1, min((int64_t)U.start + t - (int64_t)s0 * kTok, (int64_t)cnt * kTok - 1));
-        };
-        const int pos = relative(tok), pos0 = relative(U.first + x * A.tpt);
-        const uint32_t my = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = my + x * 128, tO = my + 256 + x * 128;
-        float* mult_s = reinterpret_cast<float*>(sm + L::mult) + x * 128;
-        bool empty = false;
-        if (A.stall_cycles > 0 && (split & 1)) {
-            empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
-            if (empty && r == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
-        }
-        if (steps > 0) {
-            // the tile's queries in e4m3 terms: a warp takes 32 rows, two at a time (half a warp each, 8 elements a lane).
-            // All 16 loads are in flight at once; the split then goes through them by shifting, in a loop small enough
-            // for a cold instruction cache.
-            const int sub = lane >> 4, col = lane & 15, first_row = quad * 32 + sub;
+    if (U.live && warp < 12) {
+        // The tiles' queries in e4m3 terms, 24 rows a softmax warp and 16 a converter, before the registers are shared
+        // out: two rows at a time (half a warp each, 8 elements a lane), all loads in flight at once.  The split then goes
+        // through them by shifting, in a loop small enough for a cold instruction cache.
+        const bool soft = warp < 8;
+        const int x = soft ? warp >> 2 : (warp - 8) >> 1;
+        const int base = soft ? (warp & 3) * 24 : 96 + (warp & 1) * 16, pairs = soft ? 12 : 8;
+        if ((x ? cB : cA) > 0) {
+            float* mult_s = reinterpret_cast<float*>(sm + L::mult) + x * 128;
+            const int sub = lane >> 4, col = lane & 15, first_row = base + sub;
             int row_tok = U.first + x * A.tpt + first_row / G, row_g = first_row % G;
             constexpr int kBatch = 4;
-            uint4 raw_q[16];
+            uint4 raw_q[12];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool in = first_row + 2 * i < A.tpt * G && row_tok < U.n;
+            for (int i = 0; i < 12; ++i) {
+                const bool in = i < pairs && first_row + 2 * i < A.tpt * G && row_tok < U.n;
                 const T* q = static_cast<const T*>(A.a.q) + (U.row0 + row_tok) * A.a.q_token +
                              ((int64_t)h * G + row_g) * A.a.q_head + 8 * col;
                 raw_q[i] = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
@@ -244,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                     }
             }
 #pragma unroll 1
-            for (int r0 = first_row; r0 < quad * 32 + 32; r0 += 2 * kBatch) {
+            for (int r0 = first_row; r0 < base + 2 * pairs; r0 += 2 * kBatch) {
                 uint32_t words[kBatch][4];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -270,14 +252,40 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 for (int i = 0; i < kBatch; ++i) factors = col == i ? split.factor(i, A.a.sm_scale_log2) : factors;
                 if (col < kBatch) mult_s[r0 + 2 * col] = factors;
 #pragma unroll
-                for (int i = 0; i + kBatch < 16; ++i) raw_q[i] = raw_q[i + kBatch];
+                for (int i = 0; i + kBatch < 12; ++i) raw_q[i] = raw_q[i + kBatch];
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bQ + x));
         }
         __syncwarp();
-        const float mult = steps > 0 ? mult_s[r] : 0.f;  // stored by this warp
+    }
+    if (!U.live) {
+        // no such unit
+    } else if (warp < 8) {
+        // ================= softmax: thread = query row =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int x = warp >> 2, quad = warp & 3;      // row tile, lane quarter
+        const int r = quad * 32 + lane;
+        const int tok = U.first + x * A.tpt + r / G;   // new token of the sequence
+        const bool there = r < A.tpt * G && tok < U.n;
+        const int steps = x ? cB : cA;
+        // the last token that the row sees, and the tile's first row, counted from this split's first token
+        auto relative = [&](int t) {
+            return (int)max((int64_t)-1, min((int64_t)U.start + t - (int64_t)s0 * kTok, (int64_t)cnt * kTok - 1));
+        };
+        const int pos = relative(tok), pos0 = relative(U.first + x * A.tpt);
+        const uint32_t my = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tS = my + x * 128, tO = my + 256 + x * 128;
+        float* mult_s = reinterpret_cast<float*>(sm + L::mult) + x * 128;
+        bool empty = false;
+        if (A.stall_cycles > 0 && (split & 1)) {
+            empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
+            if (empty && r == 0) flag(A.a.status, TQ_FLAG_TIMEOUT);
+        }
+        if (steps > 0) wait(bQ + x, 0);
+        __syncwarp();
+        const float mult = steps > 0 ? mult_s[r] : 0.f;
         // the row's place in the output waits there meanwhile: registers are what the loop lacks
         reinterpret_cast<int*>(mult_s)[r] = there ? (int)(U.row0 + tok) : -1;
         // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when

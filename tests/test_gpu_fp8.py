@@ -287,6 +287,40 @@ def test_prefill(tq, dtype, bs, hq, hkv, starts, news):
         at += n
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hkv,batch", [(16, 8, 24), (16, 8, 33), (32, 2, 24), (20, 20, 2)])
+def test_prefill_of_many_units(tq, dtype, hq, hkv, batch):
+    """More units than SMs, of all lengths and equal ones: sequences without new tokens, with one, behind long prefixes,
+    one with a negative start (flagged, its rows are zero), rows behind the last sequence, padding's empty sequences."""
+    gen = torch.Generator().manual_seed(53)
+    starts = torch.randint(0, 500, (batch,), generator=gen).tolist()
+    news = torch.randint(0, 1 + 3000 // batch, (batch,), generator=gen).tolist()
+    starts[0], news[0] = 0, 1500 // batch * 2
+    if batch > 2:
+        starts[1], news[1] = 700, 1
+        starts[2], news[2] = 40, 0
+        starts[3:6], news[3:6] = [128] * 3, [130] * 3
+        starts[6], news[6] = -9, 50
+        news[-1] = 0
+    lens = [max(a, 0) + n for a, n in zip(starts, news)]
+    s = Setup(tq, gen, lens, hkv, 64)
+    s.fill(lens)
+    T = sum(news)
+    q = torch.randn(T + 5, hq, D, generator=gen).to(DT[dtype]).cuda()
+    out, st = torch.full_like(q, 7), tq.new_status()
+    s.cache.prefill(q, i32(cu_of(news)), i32(starts), s.table, out=out, status=st)
+    assert st.item() == (tq.FLAG_BAD_SLOT if batch > 2 else 0)
+    assert (out[T:] == 7).all()
+    at = 0
+    for b, (a, n) in enumerate(zip(starts, news)):
+        if n and a < 0:
+            assert not out[at:at + n].any()
+        elif n:
+            k, v = R.stored(s.pool, s.scales, s.rows[b], a + n)
+            check(out[at:at + n], q[at:at + n], k, v, [a + i + 1 for i in range(n)], PREFILL)
+        at += n
+
+
 def sink_case(tq, dtype, call, gen):
     """One token that takes nearly all of the weight and 4000 others that matter together, with blocks of values of
     very different size: small weights and small scales keep their precision."""
