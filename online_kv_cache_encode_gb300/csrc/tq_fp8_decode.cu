@@ -24,8 +24,8 @@
 // whatever the lengths are.  An item (sequence, head) that lies in one run is
 // written directly; otherwise each run leaves a partial (reference, sum,
 // accumulator) and the last run to arrive joins them in their order, so results
-// do not depend on timing.  64 sequences of 1K-16K tokens, 8 KV heads: 188 us,
-// 0.86 of HBM; 32K tokens, 8 heads: 22 us, of which 13 stream (0.75).
+// do not depend on timing.  64 sequences of 1K-16K tokens, 8 KV heads: 192 us,
+// 0.84 of HBM; 32K tokens, 8 heads: 22 us, of which 13 stream (0.75).
 //
 // Warps: 0-7 softmax and accumulation (thread = token of the tile for the
 // scores, = dim for the output, the two warpgroups taking half of the columns
