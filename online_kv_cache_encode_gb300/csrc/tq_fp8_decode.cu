@@ -10,7 +10,8 @@
 // own (N = NT * GP, padded to 16), so nothing shares a range with anything:
 // 2 terms hold a bf16 query exactly (8 significant bits, to 2^-22 of the row's
 // largest element) and a weight to 2^-8, the rounding of a bf16 output; fp16
-// takes 3 terms, 2^-12.  Key scales multiply the scores, value scales the
+// takes 3 terms, 2^-12 (tiles whose value scales lie far apart are weighed in
+// fp32 instead).  Key scales multiply the scores, value scales the
 // weights (both powers of two).  The weights of a tile are taken against a
 // reference near its own maximum, not the running one, and a tile's output
 // leaves tensor memory and is joined in fp32 registers: the tokens behind one
@@ -48,7 +49,8 @@ constexpr int kPagesMax = kTile / 16;
 constexpr int kDecWarps = 12;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr float kPScale = 256.f;      // weights are coded as p * 2^8 <= 430 (e4m3's largest value is 448)
-constexpr int kWideSpread = 6;        // octaves between a tile's value scales beyond which its weights get their own range
+constexpr int kWideSpread = 6;        // octaves between a tile's value scales beyond which it is weighed in fp32
+constexpr int kLeastValueExp = -98;   // blocks below hold values under 2^-89 only: they make no tile wide
 
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -95,13 +97,12 @@ struct DecLayout {
     static constexpr int q_bytes = N * kHeadDim;
     static constexpr int p = kStages * 2 * kSide;
     static constexpr int q = p + 2 * p_bytes;
-    static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales (wide: exponents) [16 each]
+    static constexpr int meta = q + QB * q_bytes;           // per stage: key scales, relative value scales (wide: exponents - 20) [16 each]
     static constexpr int okm = meta + kStages * 2 * kPagesMax * 4;  // per stage: pages there (bit 31: wide), largest value exponent
     static constexpr int mult = okm + kStages * 8;          // per query buffer: [GP]
     static constexpr int top = (mult + QB * GP * 4 + 15) / 16 * 16;  // [2][8 warps][GP] maxima
     static constexpr int sums = top + 2 * 8 * GP * 4;       // [8 warps][GP]
-    static constexpr int own = sums + 8 * GP * 4;           // [8 warps][2][GP] output factors of wide tiles
-    static constexpr int bars = (own + 8 * 2 * GP * 4 + 7) / 8 * 8;
+    static constexpr int bars = sums + 8 * GP * 4;
     static constexpr int nbars = 3 * kStages + 6 + 2 * QB + 1;
     static constexpr int misc = bars + 8 * nbars;           // tmem address, last-arrival word
     static constexpr int total = misc + 16;
@@ -110,6 +111,7 @@ struct DecLayout {
     static_assert(p % 1024 == 0 && q % 1024 == 0 && q_bytes % 1024 == 0, "swizzled rows and 16-byte pieces");
     static_assert(meta % 16 == 0 && top % 16 == 0 && bars % 8 == 0 && misc % 8 == 0, "vector accesses");
     static_assert(smem <= kSmemLimit, "decode does not fit in shared memory");
+    static_assert(2 * p_bytes >= kTile * GP * 4, "a wide tile's fp32 weights take both weight buffers");
 };
 
 constexpr int kPartFloats = 16 * kHeadDim + 32;  // a partial: accumulators [GP][128], (max, sum) [GP]
@@ -330,19 +332,19 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                 if (lane == 0) mbar_arrive(bar(bQ + qb));
             }
             const int e = id >= 0 ? fp8_exp_of(s.y) : -1000;
-            int emax = e, emin = id >= 0 ? e : 1000;
+            int emax = e, emin = e >= kLeastValueExp ? e : 1000;
 #pragma unroll
             for (int o = 8; o; o >>= 1) {  // (lanes 0-15 hold the blocks)
                 emax = max(emax, __shfl_xor_sync(0xFFFFFFFFu, emax, o));
                 emin = min(emin, __shfl_xor_sync(0xFFFFFFFFu, emin, o));
             }
             const unsigned there = __ballot_sync(0xFFFFFFFFu, id >= 0);
-            const bool wide = emax - emin > kWideSpread;  // (without blocks emin > emax)
+            const bool wide = emax - emin > kWideSpread;  // (without such blocks emin > emax)
             if (ph > 0) wait(bE + st, (ph - 1) & 1);
             float* m = reinterpret_cast<float*>(sm + L::meta) + st * 2 * kPagesMax;
             if (lane < 16) {
                 m[lane] = s.x;
-                m[16 + lane] = id < 0 ? 0.f : wide ? (float)(e - emax) : fp8_pow2(e - emax);
+                m[16 + lane] = id < 0 ? 0.f : wide ? (float)(e - 20) : e - emax < -100 ? 0.f : fp8_pow2(e - emax);
             }
             if (lane == 0) {
                 int* o = reinterpret_cast<int*>(sm + L::okm) + 2 * st;
@@ -438,7 +440,6 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         const int dim = quad * 32 + lane;   // output dim
         int* last_s = reinterpret_cast<int*>(sm + L::misc + 8);
         float* sums_s = reinterpret_cast<float*>(sm + L::sums);
-        float* own_s = reinterpret_cast<float*>(sm + L::own) + warp * 2 * GP;
         bool empty = false;  // test hook: this CTA's partials are empty
         if (A.stall_cycles > 0 && (blockIdx.x & 1)) {
             empty = !mbar_wait_for(bar(bNever), 0, A.stall_cycles);
@@ -459,7 +460,6 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             const int qb = i % L::QB;
             const int n = min(w.nt - w.ti, t1 - t);
             float ref[GP], sum[GP], acc[H], mult[GP], fac[H], vs = 0.f;
-            bool was_wide = false;  // the tile whose output comes next
             float lref[2] = {0.f, 0.f}, lrun[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < GP; ++k) ref[k] = sum[k] = 0.f;
@@ -478,7 +478,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     float x = __uint_as_float(o[(NT - 1) * H + k]);
 #pragma unroll
                     for (int j = NT - 2; j >= 0; --j) x = fmaf(x, 0.0625f, __uint_as_float(o[j * H + k]));
-                    acc[k] = fmaf(x, was_wide ? own_s[(v & 1) * GP + wg * H + k] : vs, acc[k]);
+                    acc[k] = fmaf(x, vs, acc[k]);
                 }
             };
             wait(bQ + qb, (i / L::QB) & 1);
@@ -571,30 +571,55 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                         f2_unpack(f2_mul(p, vr2), x[k], x[k + 1]);
                     }
                 }
+                auto clear_row = [&] {  // the token's weights are 0, but its slot may hold NaN codes
+                    wait(bF + st, (u / kStages) & 1);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sb + st * 2 * kSide + v_row + 16 * c), "r"(0)
+                                     : "memory");
+                };
                 if (wide) {
-                    // Value scales far apart: a block with a large one, whatever its weights are, must not take the
-                    // range of the others.  The products weight * scale get a range of their own in every column,
-                    // 2^E below the tile's (l + scale exponent has its maximum E above the reference), down to where
-                    // the output's factor is a normal number.  The scale's place holds its exponent, for any distance.
+                    // Value scales far apart: in a column's fp8 weights a block with a large scale would take the range of
+                    // the others, also in the dims where its codes are 0 and only the others count.  So the tile is weighed
+                    // in fp32, with every token's weight times its scale (2^-20 of it, as the accumulators are) whatever
+                    // the others' are.  64 sequences of 8192 tokens, 8 KV heads: 546 us with every tile like that, 182 with
+                    // none (the loop's loads bound it: 757 with 4 tokens at a time instead of 16).  The weights go through
+                    // both weight buffers, which the tensor cores have left once the last output is there.
+                    if (j > 0) take_output(u - 1);
+                    if (moved)
+#pragma unroll
+                        for (int k = 0; k < H; ++k) acc[k] *= fac[k];
+                    float* wt = reinterpret_cast<float*>(sm + L::p);
                     const float er = me[16 + pg];
-                    float most[GP];
 #pragma unroll
-                    for (int k = 0; k < GP; ++k) most[k] = redux_max(there ? l[k] + er : -INFINITY);
-                    if (lane == 0)
-#pragma unroll
-                        for (int k = 0; k < GP; ++k) sums_s[warp * GP + k] = most[k];
+                    for (int k = 0; k < GP; k += 4)
+                        *reinterpret_cast<float4*>(wt + tid * GP + k) =
+                            make_float4(ex2((l[k] - ref[k]) + er), ex2((l[k + 1] - ref[k + 1]) + er),
+                                        ex2((l[k + 2] - ref[k + 2]) + er), ex2((l[k + 3] - ref[k + 3]) + er));
+                    if (there) wait(bF + st, (u / kStages) & 1);
+                    else clear_row();
                     soft_barrier();
-                    const float least = (float)(-98 - okm[1]);
+                    float add[H];
 #pragma unroll
-                    for (int k = 0; k < GP; ++k) {
-                        float z = -INFINITY;
+                    for (int k = 0; k < H; ++k) add[k] = 0.f;
+#pragma unroll 16
+                    for (int y = 0; y < kTile; ++y) {
+                        const int at = PAIRED ? ((y & 127) >> 3) * 4096 + 2048 + ((y >> 7) * 8 + (y & 7)) * 128 : kSide + y * 128;
+                        const float c = fp8_to_float2(sm[st * 2 * kSide + at + (((dim >> 4) ^ (y & 7)) << 4) + (dim & 15)]).x;
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) z = fmaxf(z, sums_s[y * GP + k]);
-                        const float E = z == -INFINITY ? 0.f : fminf(fmaxf(ceilf(z - ref[k]), least), 0.f);
-                        x[k] = kPScale * ex2((l[k] - ref[k]) + (er - E));
-                        if (lane == k) own_s[(u & 1) * GP + k] = E == 0.f ? vs_new : fp8_pow2((int)E + okm[1] - 28);
+                        for (int k = 0; k < H; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(wt + y * GP + wg * H + k);
+                            add[k] = fmaf(f.x, c, add[k]);
+                            add[k + 1] = fmaf(f.y, c, add[k + 1]);
+                            add[k + 2] = fmaf(f.z, c, add[k + 2]);
+                            add[k + 3] = fmaf(f.w, c, add[k + 3]);
+                        }
                     }
-                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < H; ++k) acc[k] += add[k];
+#pragma unroll
+                    for (int k = 0; k < GP; ++k) x[k] = 0.f;  // (for the tensor cores, whose output then adds nothing)
+                    soft_barrier();
                 }
                 // the weights' terms: byte n of the token's 16-column rows
                 uint32_t word[N / 4];
@@ -619,23 +644,18 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sp + k * kTile * 16), "r"(word[4 * k]),
                                  "r"(word[4 * k + 1]), "r"(word[4 * k + 2]), "r"(word[4 * k + 3])
                                  : "memory");
-                if (!there) {  // the token's weights are 0, but its slot may hold NaN codes
-                    wait(bF + st, (u / kStages) & 1);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sb + st * 2 * kSide + v_row + 16 * c), "r"(0)
-                                     : "memory");
-                }
+                if (!there && !wide) clear_row();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bP + (u & 1)));
-                if (j > 0) take_output(u - 1);
-                vs = vs_new;
-                was_wide = wide;
-                if (moved)
+                if (!wide) {
+                    if (j > 0) take_output(u - 1);
+                    if (moved)
 #pragma unroll
-                    for (int k = 0; k < H; ++k) acc[k] *= fac[k];
+                        for (int k = 0; k < H; ++k) acc[k] *= fac[k];
+                }
+                vs = vs_new;
             }
             // ---- the item's end ----
             const float part_sum = sum_lanes<GP>(sum);
