@@ -518,7 +518,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 if (e > 7) {  // 2^(e + 120) is past bf16's range: the rest in a second product
                     const uint32_t f2 = (uint32_t)(e - 7 + 127) << 7, m2 = f2 | (f2 << 16);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], m2);
+                    for (int k = 0; k < 8; ++k) {
+                        // codes of 256 and more times 2^120 are past bf16: its largest value instead, as an infinity would
+                        // reach the rows that do not see the token (0 * inf is NaN)
+                        o[k] = mul_bf16x2(o[k], m2);
+                        o[k] = (o[k] & 0x80008000u) | __vminu2(o[k] & 0x7FFF7FFFu, 0x7F7F7F7Fu);
+                    }
                 }
                 const uint32_t at = dst + (2 * c) * kVSbo + (t >> 3) * kVLbo + (t & 7) * 16;
                 pre_sts128(at, o[0], o[1], o[2], o[3]);

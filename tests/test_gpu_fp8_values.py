@@ -41,7 +41,7 @@ def test_large_scales_over_codes_of_zero(tq, dtype, call, octaves, bs, hq):  # n
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("call", ["decode"])
+@pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_values_at_the_limit_that_a_row_does_not_see(tq, dtype, call):  # noqa: F811
     """A block whose scale is the largest: values of 2^128, past what bf16 holds, at later positions and any bytes behind
     the end must not reach the rows before them."""
@@ -63,7 +63,7 @@ def test_values_at_the_limit_that_a_row_does_not_see(tq, dtype, call):  # noqa: 
     check(out, q[:100], k, v, list(range(1, 101)), DECODE if call == "decode" else PREFILL)
 
 
-@pytest.mark.parametrize("call", ["decode"])
+@pytest.mark.parametrize("call", ["decode", "prefill"])
 def test_any_bytes_behind_the_end_of_a_block_of_the_largest_scale(tq, call):  # noqa: F811
     gen = torch.Generator().manual_seed(64)
     n = 37
