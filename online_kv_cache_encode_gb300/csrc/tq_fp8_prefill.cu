@@ -55,16 +55,18 @@ struct PreLayout {
     static constexpr int vb = v + 2 * 16384;            // [2] bf16 operand: 8 x 8 core matrices, MN-major
     static constexpr int meta = vb + 2 * 32768;         // [ring]: key scales [8], value scales [8] of 16 tokens each
     static constexpr int okm = meta + kMetaRing * 64;   // [ring]: groups of 16 tokens that are there
-    static constexpr int bars = okm + kMetaRing * 4 + 16 - kMetaRing * 4 % 16;
+    static constexpr int bars = okm + kMetaRing * 4;
     static constexpr int nbars = 2 + 2 * KS + 4 + 4 + 6 + 2 * kMetaRing + 1;
-    static constexpr int misc = bars + nbars * 8;
+    static constexpr int misc = bars + nbars * 8;       // tensor memory's address; the first token with a NaN in any dim
     static constexpr int mult = misc + 16;              // [256] rows' score multipliers
-    static constexpr int total = mult + 256 * 4;
-    static constexpr int smem = total + 1024;
+    static constexpr int nan = mult + 256 * 4;          // [128 dims] the first token of this split whose value is a NaN there
+    static constexpr int total = nan + kHeadDim * 4;
+    static constexpr int smem = total + 1008;           // the base is rounded up to 1 KB, from 16 bytes at least
     static_assert(k % 1024 == 0 && v % 1024 == 0 && vb % 1024 == 0 && meta % 16 == 0 && bars % 8 == 0, "alignment");
     static_assert(smem <= kSmemLimit, "prefill does not fit in shared memory");
 };
-// V's operand: 8 tokens x 8 dims core matrices of 128 bytes, token groups 128 bytes apart, dim groups 2048
+// V's operand: 8 tokens x 8 dims core matrices of 128 bytes, token groups 128 bytes apart, dim groups 2048; the dims of
+// every four in the order 0, 2, 1, 3, as a word of codes is taken apart with the fewest instructions
 constexpr uint32_t kVLbo = 128, kVSbo = 2048;
 
 struct PreArgs {
@@ -116,6 +118,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// Notes the codes of NaN among the 32 tokens of a step that converter `cw` has: in `first` the first token of each dim that
+// holds one, in `any` of all dims, counted from the split's first token (t0 is the step's).  Rare, and out of line: inlined
+// it made the loop that calls it slower (a chunk of 4096 at 12288: 1368 us against 1345).
+__device__ __noinline__ void note_nan(const uint8_t* codes, const int* exps, int* first, int* any, int cw, int t0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = lane; i < 32 * kHeadDim; i += 32) {
+        const int t = cw * 32 + (i >> 7), d = i & 127;
+        const uint8_t code = codes[t * 128 + (((d >> 4) ^ (t & 7)) << 4) + (d & 15)];
+        if ((code & 127) == 127 && exps[t >> 4] != INT_MIN) {
+            atomicMin(first + d, t0 + t);
+            atomicMin(any, t0 + t);
+        }
+    }
+}
+
 template <typename T, int NT, int NP>  // NP: bf16 operands of the weights
 __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs A, const __grid_constant__ CUtensorMap map) {
     using L = PreLayout<NT>;
@@ -155,6 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         mbar_init(bar(bNever), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    int* nan_s = reinterpret_cast<int*>(sm + L::nan);
+    int* any_nan = reinterpret_cast<int*>(sm + L::misc + 4);
+    if (tid < kHeadDim) nan_s[tid] = INT_MAX;
+    if (tid == kHeadDim) *any_nan = INT_MAX;
     if (warp == 12 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     if (warp == 13) tc::tmem_alloc<512>(sb + L::misc);
     tc::fence_before_sync();
@@ -447,6 +469,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             __syncwarp();
         };
         auto piece = [&](int i) { return stage + lane * 256 + ((i ^ (lane & 7)) << 4); };
+        auto swap_dims = [](uint32_t (&o)[16]) {  // the columns are dims 0, 2, 1, 3 of every four
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const uint32_t y = o[i + 1];
+                o[i + 1] = o[i + 2];
+                o[i + 2] = y;
+            }
+        };
+        // a dim is NaN from the first token on that has a NaN there: in the staged rows, dims d0 .. of `size` bytes
+        auto spoil = [&](int d0, int n, int size) {
+#pragma unroll 1
+            for (int d = *any_nan <= pos ? 0 : n; d < n; ++d)
+                if (nan_s[d0 + d] <= pos) {
+                    const uint32_t at = piece(d * size >> 4) + (d * size & 15);
+                    if (size == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0x7FFF) : "memory");
+                    else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0x7FFFFFFF) : "memory");
+                }
+        };
         if (A.splits == 1) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             T* out = static_cast<T*>(A.a.out) + ((int64_t)row * A.a.hq + (int64_t)h2 * A.a.group + r % A.a.group) * kHeadDim;
@@ -456,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                     uint32_t o[16];
                     tmem_ld<16>(tO + 16 * c, o);
                     tmem_ready<16>(o);
+                    swap_dims(o);
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -463,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                     pre_sts128(piece(2 * c), w[0], w[1], w[2], w[3]);
                     pre_sts128(piece(2 * c + 1), w[4], w[5], w[6], w[7]);
                 }
+                spoil(0, kHeadDim, 2);
                 leave(row >= 0 && !empty ? reinterpret_cast<char*>(out) : nullptr);
             }
         } else {
@@ -480,9 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                         uint32_t o[16];
                         tmem_ld<16>(tO + 64 * half + 16 * c, o);
                         tmem_ready<16>(o);
+                        swap_dims(o);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) pre_sts128(piece(4 * c + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
+                    spoil(64 * half, 64, 4);
                     leave(part ? part + 256 * half : nullptr);
                 }
         }
@@ -497,8 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             if (u > 1) wait(bBe + b, ((u - 2) >> 1) & 1);
             const int* vs = reinterpret_cast<const int*>(sm + L::meta + mi * 64 + 32);
             const uint32_t src = sb + L::v + b * 16384, dst = sb + L::vb + b * 32768;
-            // a warp converts 32 tokens: 8 of them by 4 pieces of 16 codes at a time
-#pragma unroll 1
+            uint32_t most = 0;  // largest magnitudes, in either half: a NaN's is 0x7F0
+            // a warp converts 32 tokens: 8 of them by 4 pieces of 16 codes at a time (unrolled by measurement: twice is 2 %
+            // faster than once with two query terms, 4 % slower with three)
+#pragma unroll (NT == 2 ? 2 : 1)
             for (int i = 0; i < 8; ++i) {
                 const int t = cw * 32 + (i >> 1) * 8 + (lane & 7), c = (i & 1) * 4 + (lane >> 3);
                 const uint4 v4 = lds128(src + t * 128 + ((c ^ (t & 7)) << 4));
@@ -511,9 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 uint32_t o[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t a = prmt(w[k], 0, 0x1404), z = prmt(w[k], 0, 0x3424);
-                    o[2 * k] = mul_bf16x2((a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), m1);
-                    o[2 * k + 1] = mul_bf16x2((z & 0x80008000u) | ((z & 0x7F007F00u) >> 4), m1);
+                    // dims 0 and 2, 1 and 3 of the word's four: the operand's columns hold them in that order
+                    const uint32_t even = (w[k] << 4) & 0x07F007F0u, odd = (w[k] >> 4) & 0x07F007F0u;
+                    o[2 * k] = mul_bf16x2(((w[k] << 8) & 0x80008000u) | even, m1);
+                    o[2 * k + 1] = mul_bf16x2((w[k] & 0x80008000u) | odd, m1);
+                    most = __vimax3_u16x2(most, even, odd);
                 }
                 if (e > 7) {  // 2^(e + 120) is past bf16's range: the rest in a second product
                     const uint32_t f2 = (uint32_t)(e - 7 + 127) << 7, m2 = f2 | (f2 << 16);
@@ -529,6 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 pre_sts128(at, o[0], o[1], o[2], o[3]);
                 pre_sts128(at + kVSbo, o[4], o[5], o[6], o[7]);
             }
+            // A NaN (0x7F or 0xFF: tq_fp8_write stores none, but a pool may come from elsewhere) is 480 in the operand, which
+            // does no harm to the rows that do not see it; the rows' end makes it NaN for those that do.
+            if (__any_sync(0xFFFFFFFFu, (most & 0xFFFFu) == 0x7F0u || (most >> 16) == 0x7F0u))
+                note_nan(sm + L::v + b * 16384, vs, nan_s, any_nan, cw, u * kTok);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {

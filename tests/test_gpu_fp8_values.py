@@ -5,9 +5,81 @@ import pytest
 import torch
 
 from tests import fp8_reference as R
-from tests.test_gpu_fp8 import D, DECODE, DT, PREFILL, Setup, check, i32, tq  # noqa: F401
+from tests.test_gpu_fp8 import D, DECODE, DT, PREFILL, Setup, check, cu_of, i32, tq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def clean(x):
+    return torch.where(torch.isnan(x), torch.zeros_like(x), x)
+
+
+def check_nan(out, q, k, v, limits, floor):
+    """Row i's element d is NaN where the row sees a NaN in dim d of the values, the whole row where it sees one in the
+    keys, by KV head; every other element is what it is without them."""
+    group = q.shape[1] // k.shape[0]
+    see = torch.arange(k.shape[1], device=q.device)[None, :] < torch.as_tensor(limits, device=q.device)[:, None]
+    nan = (see[:, None, :, None] & (torch.isnan(v) | torch.isnan(k).any(-1, keepdim=True))[None]).any(2)
+    nan = nan.repeat_interleave(group, 1)
+    assert torch.equal(torch.isnan(out), nan)
+    want = R.attend(q, clean(k), clean(v), limits, 1 / math.sqrt(D), None, floor)[0]
+    check(torch.where(nan, want.to(out.dtype), out), q, clean(k), clean(v), limits, floor)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bs,hq,hkv,start,new", [
+    (16, 8, 2, 0, 420),      # a unit sees the tokens that others of its rows do not
+    (64, 5, 1, 2900, 7),     # the tokens split among many CTAs
+    (32, 20, 20, 130, 150),
+])
+def test_nan_codes(tq, dtype, bs, hq, hkv, start, new):  # noqa: F811
+    """A pool that another program filled may hold codes of NaN at positions that are read: they are NaN to every call,
+    in the rows that see them and in no others."""
+    gen = torch.Generator().manual_seed(61)
+    n = start + new
+    s = Setup(tq, gen, [n], hkv, bs)
+    s.fill([n])
+    last = [n - 1 - x for x in (0, 1, 5, new // 2, new - 1) if x < new]
+    for i, p in enumerate(last + [start // 2, start // 3 + 17]):
+        blk = s.rows[0][p // bs]
+        s.pool[blk, 0, 1, p % bs, (37 * i + 3) % D] = 0x7F if i % 2 else 0xFF
+        if i == 3:
+            s.pool[blk, hkv - 1, 1, p % bs, 64:80] = 0x7F
+    if hkv > 1:
+        p = start + new // 3
+        s.pool[s.rows[0][p // bs], 1, 0, p % bs, 9] = 0x7F
+    q = torch.randn(new, hq, D, generator=gen).to(DT[dtype]).cuda()
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    out = s.cache.prefill(q, i32([0, new]), i32([start]), s.table)
+    check_nan(out, q, k, v, [start + i + 1 for i in range(new)], PREFILL)
+    lens = [n, start + 1, n - 2]
+    out = s.cache.decode(q[:3], s.table.repeat(3, 1), i32(lens))
+    check_nan(out, q[:3], k, v, lens, DECODE)
+    got = s.cache.read(i32([0, n]), i32([0]), s.table, n, torch.float32)
+    for x, want in zip(got, (k, v)):
+        assert torch.equal(torch.nan_to_num(x.double(), nan=7e7), torch.nan_to_num(want.permute(1, 0, 2), nan=7e7))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_nan_codes_that_no_row_sees(tq, dtype):  # noqa: F811
+    """Codes of NaN behind the sequence's end, in blocks that the table does not name and in the other sequence's."""
+    gen = torch.Generator().manual_seed(62)
+    starts, news = [0, 77], [133, 200]
+    lens = [a + b for a, b in zip(starts, news)]
+    s = Setup(tq, gen, lens, 2, 16)
+    s.fill(lens)
+    for b, n in enumerate(lens):
+        s.pool[s.rows[b][n // 16], :, :, n % 16:] = 0x7F
+    s.pool[s.free] = 0xFF
+    s.pool[s.rows[0][3], 1, 1, 5, 8] = 0x7F      # position 53 of sequence 0
+    q = torch.randn(sum(news), 4, D, generator=gen).to(DT[dtype]).cuda()
+    out = s.cache.prefill(q, i32(cu_of(news)), i32(starts), s.table)
+    one = s.cache.decode(q[:2], s.table, i32(lens))
+    for b, (a, n) in enumerate(zip(starts, news)):
+        at = cu_of(news)[b]
+        k, v = R.stored(s.pool, s.scales, s.rows[b], a + n)
+        check_nan(out[at:at + n], q[at:at + n], k, v, [a + i + 1 for i in range(n)], PREFILL)
+        check_nan(one[b:b + 1], q[b:b + 1], k, v, [a + n], DECODE)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
