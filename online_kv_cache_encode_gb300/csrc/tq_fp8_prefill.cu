@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::misc);
+    // (The next grid is not let in early: CTAs that wait for this one's end cost it more than their start takes, 117 us
+    // against 106 for a ragged fp16 batch of 300 units called again and again, 76 against 72 for 64 tokens at 32704.)
     grid_dependency_wait();
-    grid_launch_dependents();
 
     // ---- the unit, its row tiles and this split's tokens ----
     // heads and splits run fastest; the units go from the last back, as those attend to the most tokens
