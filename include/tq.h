@@ -469,15 +469,17 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* cache, void* K, void* V, tq_dty
  * behind a sequence's end may hold any bytes.  num_q_heads is a multiple of
  * num_kv_heads, at most 128 times it.  sm_scale: positive and finite.
  * workspace: device, 256-byte aligned, at least
- * tq_fp8_decode_workspace_bytes(...) bytes, zero-filled once before its first
- * use; each call leaves its counters at zero again, also one that reported
- * TQ_FLAG_TIMEOUT, and calls of all shapes on one device may follow one another
- * on a workspace.  Two calls in flight at once, replays of captured ones among
+ * tq_fp8_decode_workspace_bytes(...) bytes, of any contents before the offset
+ * tq_fp8_decode_counters_offset(cache), which depends on the device only, and
+ * zero-filled from there on before its first use; each call leaves its counters
+ * at zero again, also one that reported TQ_FLAG_TIMEOUT, and calls of all
+ * shapes on one device may follow one another on a workspace.  Two calls in flight at once, replays of captured ones among
  * them, must not share a workspace.
  * Stored values and queries of 2^-90 .. 2^90 keep the precision of the
  * accumulators (fp32, scaled by up to 2^-24); a query row that holds a NaN or
  * an infinity gives NaN in its own output row only. */
 TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* cache, int batch, int num_q_heads);
+TQ_API size_t tq_fp8_decode_counters_offset(const tq_fp8_cache* cache);
 TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_seq_stride,
                                          int64_t q_head_stride, int batch, int num_q_heads, const int32_t* block_table,
                                          int max_blocks_per_seq, const int32_t* lens, float sm_scale, void* out,
@@ -489,7 +491,7 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* 
  * [num_tokens, num_q_heads, d] packed like K and V; workspace: at least
  * tq_fp8_prefill_workspace_bytes(...) bytes of any contents, 256-byte aligned,
  * not shared by two calls in flight at once (a decode call that takes it over
- * needs it zero-filled again). */
+ * needs its counters zero-filled again). */
 TQ_API size_t tq_fp8_prefill_workspace_bytes(const tq_fp8_cache* cache, int64_t num_tokens, int batch, int num_q_heads);
 TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype,
                                           int64_t q_token_stride, int64_t q_head_stride, int64_t num_tokens, int batch,

@@ -72,6 +72,7 @@ int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
 bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g, int rows);
 bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_blocks);  // tiles are counted in 32 bits
 size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group);
+size_t fp8_decode_counters_at(const Fp8Geometry& g);  // the workspace's part that has to be zero starts there
 int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
 bool fp8_prefill_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);  // the grid fits 32 bits
 size_t fp8_prefill_workspace(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);

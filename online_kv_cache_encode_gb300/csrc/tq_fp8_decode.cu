@@ -800,6 +800,8 @@ size_t fp8_decode_workspace(const Fp8Geometry& g, int batch, int group) {
     return partial_bytes(g) + counter_bytes(batch, g.hkv, group);
 }
 
+size_t fp8_decode_counters_at(const Fp8Geometry& g) { return partial_bytes(g); }
+
 int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream) {
     DecArgs d{};
     d.a = a;

@@ -202,6 +202,8 @@ TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* c, int batch, in
     return fp8_decode_workspace(c->g, batch, num_q_heads / c->g.hkv);
 }
 
+TQ_API size_t tq_fp8_decode_counters_offset(const tq_fp8_cache* c) { return c ? fp8_decode_counters_at(c->g) : 0; }
+
 TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64_t q_seq_stride,
                                          int64_t q_head_stride, int batch, int num_q_heads, const int32_t* block_table,
                                          int max_blocks_per_seq, const int32_t* lens, float sm_scale, void* out,

@@ -52,6 +52,7 @@ SIGNATURES = {
     "tq_fp8_write": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I, _P, _P]),
     "tq_fp8_read": (_I, [_P, _P, _P, _I, _I64, _I, _P, _P, _P, _I, _P, _P]),
     "tq_fp8_decode_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "tq_fp8_decode_counters_offset": (_SZ, [_P]),
     "tq_fp8_decode_attention": (_I, [_P, _P, _I, _I64, _I64, _I, _I, _P, _I, _P, _F, _P, _P, _SZ, _P, _P]),
     "tq_fp8_prefill_workspace_bytes": (_SZ, [_P, _I64, _I, _I]),
     "tq_fp8_prefill_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _P, _I, _F, _P, _P, _SZ, _P, _P]),
@@ -415,6 +416,7 @@ class Fp8Cache:
                                              ctypes.byref(self._h)))
         self._ws = {}
         self._lib = lib()
+        self._counters_at = int(self._lib.tq_fp8_decode_counters_offset(self._h))
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -445,16 +447,23 @@ class Fp8Cache:
         assert h == heads and d == self.d and sd == 1 and x.get_device() == self._dev
         return (st if T > 1 else 0), (sh if h > 1 else 0)
 
+    def _new_workspace(self, kind, nbytes) -> torch.Tensor:
+        # only a decode's counters have to be zero; a captured call clears them in each replay
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.pool.device)
+        if kind == "decode":
+            ws[self._counters_at:].zero_()
+        return ws
+
     def _workspace(self, kind, key, stream, nbytes) -> torch.Tensor:
         # one for each stream, so that calls on two streams may overlap; a call
-        # that is being captured gets its own, cleared by each replay
+        # that is being captured gets its own
         if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.zeros(max(nbytes(self._h, *key), 256), dtype=torch.uint8, device=self.pool.device)
+            return self._new_workspace(kind, nbytes(self._h, *key))
         held = self._ws.get((kind, stream))
         if held is None or held[0] != key:
-            need = max(nbytes(self._h, *key), 256)
+            need = nbytes(self._h, *key)
             if held is None or held[1].numel() < need:
-                held = (key, torch.zeros(need, dtype=torch.uint8, device=self.pool.device))
+                held = (key, self._new_workspace(kind, need))
             self._ws[(kind, stream)] = held = (key, held[1])
         return held[1]
 
@@ -511,7 +520,8 @@ class Fp8Cache:
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                status: torch.Tensor | None = None) -> torch.Tensor:
         """q: [B, Hq, d] (bf16/f16, any strides of its first two dimensions); lens: int32 [B] -> out [B, Hq, d]
-        of q's type.  A workspace is kept for each stream unless one is given."""
+        of q's type.  A workspace is kept for each stream unless one is given (as tq_fp8_decode_attention wants it:
+        its counters zero before the first use)."""
         if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.decode(q, block_table, lens, sm_scale, out, workspace, status)
