@@ -263,7 +263,8 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
         advance(quarter);
         int id = t < t1 ? page_id(w, pg) : -1;
         const int n = t1 - t0;
-        for (int u = 0; u < n; u += 4) {
+        int sent = 0;  // tiles whose copies are issued: none after a wait that gave up
+        for (int u = 0; u < n && !bad; u += 4) {
             const int now = id, h = w.hs / A.nsub, b = w.b;
             const bool first = t < t1 && w.ti == 0 && w.hs == 0;
             advance(4);
@@ -272,7 +273,12 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             for (int k = 0; k < 4 && u + k < n; ++k) {
                 const int st = (u + k) % kStages, ph = (u + k) / kStages;
                 const unsigned there = __ballot_sync(0xFFFFFFFFu, quarter == k && now >= 0);
-                if (ph > 0) wait(bE + st, (ph - 1) & 1);
+                if (ph > 0) {
+                    wait(bE + st, (ph - 1) & 1);
+                    bad = __any_sync(0xFFFFFFFFu, bad);
+                    if (bad) break;
+                }
+                sent = u + k + 1;
                 if (lane == 0) mbar_arrive_tx(bar(bF + st), (uint32_t)__popc(there) * bytes);
                 __syncwarp();
                 if (quarter == k && now >= 0) tma_page(sb + st * 2 * kSide + at, &map, row, bar(bF + st));
@@ -284,7 +290,7 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             }
         }
         // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
-        for (int u = max(0, n - kStages); u < n; ++u) mbar_wait(bar(bF + u % kStages), (u / kStages) & 1);
+        for (int u = max(0, sent - kStages); u < sent; ++u) mbar_wait(bar(bF + u % kStages), (u / kStages) & 1);
     } else if (warp == 11) {
         // ================= queries and scales =================
         Walk w = w0;
@@ -427,6 +433,9 @@ fp8_decode_kernel(const DecArgs A, const __grid_constant__ CUtensorMap map) {
             if (did) since = clock64();
             else if (__any_sync(0xFFFFFFFFu, clock64() - since > kWaitCycles)) bad = true;
         }
+        // products may be in flight where a wait gave up: they too end before the memory is given back
+        if (u > 0) mbar_wait(bar(bS + ((u - 1) & 1)), ((u - 1) >> 1) & 1);
+        if (v > 0) mbar_wait(bar(bO + ((v - 1) & 1)), ((v - 1) >> 1) & 1);
         __syncwarp();
     } else {
         // ================= softmax and accumulation =================

@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             const bool mine = lane < 16 && pg < pages;
             const int per = g.bs >> 4;  // groups of 16 tokens in a block
             int id = mine && cnt > 0 ? block_of(0, pg * per) : -1;
+            int sent_k = 0, sent_v = 0;  // steps whose copies are issued: none after a wait that gave up
             for (int u = 0; u < cnt; ++u) {
                 const int now = id;
                 id = mine && u + 1 < cnt ? block_of(u + 1, pg * per) : -1;
@@ -606,19 +607,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 const unsigned kmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 0), vmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 1);
                 const int ks = u % L::KS;
                 if (u >= L::KS) wait(bKe + ks, (u / L::KS - 1) & 1);
+                sent_k = u + 1;
                 if (lane == 0) mbar_arrive_tx(bar(bK + ks), (uint32_t)__popc(kmask) * bytes);
                 __syncwarp();
                 if (now >= 0 && side == 0) tma_page(sb + L::k + ks * 16384 + pg * bytes, &map, row, bar(bK + ks));
                 if (u > 1) wait(bVe + (u & 1), ((u - 2) >> 1) & 1);
+                sent_v = u + 1;
                 if (lane == 0) mbar_arrive_tx(bar(bV + (u & 1)), (uint32_t)__popc(vmask) * bytes);
                 __syncwarp();
                 if (now >= 0 && side == 1) tma_page(sb + L::v + (u & 1) * 16384 + pg * bytes, &map, row, bar(bV + (u & 1)));
                 if (now == -2) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+                if (u > 1 && __any_sync(0xFFFFFFFFu, bad)) break;
             }
             if (lane == 0 && (U.start < 0 || (int64_t)U.start + min(U.n, U.first + 2 * A.tpt) > cap)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
             // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
-            for (int u = max(0, cnt - L::KS); u < cnt; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
-            for (int u = max(0, cnt - 2); u < cnt; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
+            for (int u = max(0, sent_k - L::KS); u < sent_k; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
+            for (int u = max(0, sent_v - 2); u < sent_v; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
         } else if (warp == 14) {
             // ================= scales of every 16 tokens =================
             for (int u = 0; u < cnt; ++u) {
@@ -698,6 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             if (cnt > 0) {
                 if (cnt - 1 < cB) values(1, cnt - 1);
                 release(cnt - 1);
+                // products may be in flight where a wait gave up: they too end before the memory is given back
+                mbar_wait(bar(bBe + ((cnt - 1) & 1)), ((cnt - 1) >> 1) & 1);
             }
         }
     }
