@@ -400,7 +400,10 @@ TQ_API tq_status tq_decode_attention_noalloc(const tq_cache* cache, const void* 
  *   codes   device uint8 [num_blocks, num_kv_heads, 2, block_size, d], side 0
  *           the keys, side 1 the values
  *   scales  device fp32  [num_blocks, num_kv_heads, 2], powers of two
- * A stored value is code * scale.
+ * A stored value is code * scale.  tq_fp8_write stores no NaN, but a pool that
+ * another program filled may hold the codes 0x7F and 0xFF: a NaN among the
+ * values makes its dim NaN in every row of attention that sees its position,
+ * one among the keys the whole row, and neither any other row.
  *
  * The ragged calls take a batch of sequences packed one behind the other: rows
  * cu_tokens[b] .. cu_tokens[b + 1] - 1 of the packed tensors (device int32
@@ -473,11 +476,16 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* cache, void* K, void* V, tq_dty
  * tq_fp8_decode_counters_offset(cache), which depends on the device only, and
  * zero-filled from there on before its first use; each call leaves its counters
  * at zero again, also one that reported TQ_FLAG_TIMEOUT, and calls of all
- * shapes on one device may follow one another on a workspace.  Two calls in flight at once, replays of captured ones among
- * them, must not share a workspace.
+ * shapes on one device may follow one another on a workspace.  Two calls in
+ * flight at once, replays of captured ones among them, must not share a
+ * workspace.
  * Stored values and queries of 2^-90 .. 2^90 keep the precision of the
- * accumulators (fp32, scaled by up to 2^-24); a query row that holds a NaN or
- * an infinity gives NaN in its own output row only. */
+ * accumulators (fp32, scaled by up to 2^-24) while the scores fit fp32.  Each
+ * weight is rounded to 2^-8 of itself (fp16 queries: 2^-12), a small one to
+ * 2^-16 (2^-20) of the largest among its 256 tokens or 2^-40 (2^-44) of the
+ * largest of all, at most 2^6 times that where the 256 tokens' value scales
+ * differ.  A query row that holds a NaN or an infinity gives NaN in its own
+ * output row only. */
 TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* cache, int batch, int num_q_heads);
 TQ_API size_t tq_fp8_decode_counters_offset(const tq_fp8_cache* cache);
 TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_seq_stride,
@@ -488,7 +496,10 @@ TQ_API tq_status tq_fp8_decode_attention(const tq_fp8_cache* cache, const void* 
 /* Causal attention of the new tokens of a ragged batch, whose keys and values
  * are in the cache already (tq_fp8_write first): the query row of position p
  * attends over positions 0 .. p.  q and out as for the decode call, with rows
- * [num_tokens, num_q_heads, d] packed like K and V; workspace: at least
+ * [num_tokens, num_q_heads, d] packed like K and V.  Each weight is rounded to
+ * 2^-8 of itself (2^-16 for fp16 queries) whatever the others are; a query's
+ * elements below 2^-18 of its row's largest vanish; stored values past bf16's
+ * largest, 2^128 (1 - 2^-8), count as that.  workspace: at least
  * tq_fp8_prefill_workspace_bytes(...) bytes of any contents, 256-byte aligned,
  * not shared by two calls in flight at once (a decode call that takes it over
  * needs its counters zero-filled again). */

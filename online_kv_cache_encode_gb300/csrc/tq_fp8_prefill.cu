@@ -8,7 +8,7 @@
 //   O [128 rows x 128 dims]  += P . V      kind::f16 with bf16 operands
 // K goes to the tensor cores as its codes.  A query row is split into e4m3
 // terms that add up in one accumulator, x = h1 + h2 (+ h3), scaled so that its
-// largest element lies in [224, 448]: 2 terms are a bf16 query's 8 bits (3 an
+// largest element lies in (224, 448]: 2 terms are a bf16 query's 8 bits (3 an
 // fp16 one's 11), down to steps of 2^-9, 2^-17.8 of the row's largest element.
 // Two passes of fp8 cost what one of bf16 does, and K needs no conversion.
 // V's codes times their block's scale are exact in bf16, and bf16 weights keep
@@ -24,9 +24,10 @@
 // the same K and V.
 //
 // Warps: 0-3 softmax of A, 4-7 of B (thread = row), 8-11 V's conversion (these
-// twelve split the queries first), 12 TMA, 13 MMA, 14 scales.  Tensor memory: S_A, S_B (their weights overwrite
-// them), O_A, O_B, 128 columns each.  O is rescaled in place where a row's
-// reference rises, which hardly happens after the first step.
+// twelve split the queries first), 12 TMA, 13 MMA, 14 scales.  Tensor memory:
+// S_A, S_B (their weights overwrite them), O_A, O_B, 128 columns each.  O is
+// rescaled in place where a row's reference rises, which hardly happens after
+// the first step.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -312,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         // the row's place in the output waits there meanwhile: registers are what the loop lacks
         reinterpret_cast<int*>(mult_s)[r] = there ? (int)(U.row0 + tok) : -1;
         // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when
-        // a weight exceeds 1, that is when the 128 weights of a step add up to more than 128: bf16 and fp32 keep their
-        // precision at any size, the sum is needed anyway, and no maximum is formed otherwise (which took a fifth of the
-        // step).  The scores are still in tensor memory then, and the step is weighed again.  A row that has seen no
+        // the 128 weights of a step add up to more than 128 (some weight is above 1 then; where it is not raised each is at
+        // most 128): bf16 and fp32 keep their precision at any size, the sum is needed anyway, and no maximum is formed
+        // otherwise (which took a fifth of the step).  The scores are still in tensor memory then, and the step is weighed again.  A row that has seen no
         // token yet has no reference.
         float m = there ? -INFINITY : 0.f;
         uint64_t acc = f2_pack(0.f, 0.f);
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             const bool mine = lane < 16 && pg < pages;
             const int per = g.bs >> 4;  // groups of 16 tokens in a block
             int id = mine && cnt > 0 ? block_of(0, pg * per) : -1;
-            int sent_k = 0, sent_v = 0;  // steps whose copies are issued: none after a wait that gave up
+            int sent = 0;  // steps whose copies are issued: none behind one whose wait gave up
             for (int u = 0; u < cnt; ++u) {
                 const int now = id;
                 id = mine && u + 1 < cnt ? block_of(u + 1, pg * per) : -1;
@@ -607,12 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 const unsigned kmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 0), vmask = __ballot_sync(0xFFFFFFFFu, now >= 0 && side == 1);
                 const int ks = u % L::KS;
                 if (u >= L::KS) wait(bKe + ks, (u / L::KS - 1) & 1);
-                sent_k = u + 1;
                 if (lane == 0) mbar_arrive_tx(bar(bK + ks), (uint32_t)__popc(kmask) * bytes);
                 __syncwarp();
                 if (now >= 0 && side == 0) tma_page(sb + L::k + ks * 16384 + pg * bytes, &map, row, bar(bK + ks));
                 if (u > 1) wait(bVe + (u & 1), ((u - 2) >> 1) & 1);
-                sent_v = u + 1;
+                sent = u + 1;
                 if (lane == 0) mbar_arrive_tx(bar(bV + (u & 1)), (uint32_t)__popc(vmask) * bytes);
                 __syncwarp();
                 if (now >= 0 && side == 1) tma_page(sb + L::v + (u & 1) * 16384 + pg * bytes, &map, row, bar(bV + (u & 1)));
@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             }
             if (lane == 0 && (U.start < 0 || (int64_t)U.start + min(U.n, U.first + 2 * A.tpt) > cap)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
             // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
-            for (int u = max(0, sent_k - L::KS); u < sent_k; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
-            for (int u = max(0, sent_v - 2); u < sent_v; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
+            for (int u = max(0, sent - L::KS); u < sent; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
+            for (int u = max(0, sent - 2); u < sent; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
         } else if (warp == 14) {
             // ================= scales of every 16 tokens =================
             for (int u = 0; u < cnt; ++u) {

@@ -394,6 +394,10 @@ class Fp8Cache:
     block_table int32 [B, max_blocks], all on the device: rows cu_tokens[b] ..
     cu_tokens[b + 1] - 1 of the packed tensors are positions start[b] .. of
     sequence b.
+
+    Rows of d elements (of K, V and q) are contiguous and start on 16-byte
+    boundaries; their token and head strides are free otherwise.  The calls
+    record no gradient: their results are detached from q, K and V.
     """
 
     def __init__(self, num_blocks: int, num_kv_heads: int, block_size: int = 16, d: int = 128,
@@ -469,7 +473,7 @@ class Fp8Cache:
 
     def write(self, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
               block_table: torch.Tensor, status: torch.Tensor | None = None) -> None:
-        """Quantise K, V ([T, num_kv_heads, d], f32/bf16/f16, any token and head strides) into the cache."""
+        """Quantise K, V ([T, num_kv_heads, d], f32/bf16/f16, strided rows on 16-byte boundaries) into the cache."""
         if torch._C._cuda_getDevice() != self._dev:
             with torch.cuda.device(self._dev):
                 return self.write(K, V, cu_tokens, start, block_table, status)
@@ -519,7 +523,7 @@ class Fp8Cache:
     def decode(self, q: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, sm_scale: float | None = None,
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                status: torch.Tensor | None = None) -> torch.Tensor:
-        """q: [B, Hq, d] (bf16/f16, any strides of its first two dimensions); lens: int32 [B] -> out [B, Hq, d]
+        """q: [B, Hq, d] (bf16/f16, strided rows on 16-byte boundaries); lens: int32 [B] -> out [B, Hq, d]
         of q's type.  A workspace is kept for each stream unless one is given (as tq_fp8_decode_attention wants it:
         its counters zero before the first use)."""
         if torch._C._cuda_getDevice() != self._dev:
