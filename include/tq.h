@@ -510,6 +510,117 @@ TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* cache, const void*
                                           const int32_t* block_table, int max_blocks_per_seq, float sm_scale, void* out,
                                           void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------- */
+/* Rotary positions                                                        */
+/* ---------------------------------------------------------------------- */
+
+/* The first `rot` dims of a head are pairs, which a position p rotates: pair
+ * j's (a, b) becomes
+ *   (a c - b s, b c + a s),  c = m cos(p f_j),  s = m sin(p f_j),
+ * with frequencies f_j and a magnitude m; the dims behind stay as they are.
+ * TQ_ROTARY_HALF pairs dim j with j + rot / 2, TQ_ROTARY_INTERLEAVED dim 2 j
+ * with 2 j + 1.  Every cache of this library stores what it is given, so keys
+ * are rotated before they are encoded or written, or by tq_fp8_append on the
+ * way, and queries before they attend.
+ *
+ * The angles come from a table that the caller owns, device fp32
+ * [num_positions, 2, rot / 2]: a position's m cos(p f_j), then its m sin(p
+ * f_j).  tq_rotary_table fills one, or the caller does.  rot: a multiple of
+ * 16, at most 256; the table: 16-byte aligned. */
+typedef enum { TQ_ROTARY_HALF = 0, TQ_ROTARY_INTERLEAVED = 1 } tq_rotary_layout;
+
+/* How frequencies change for contexts longer than a model was trained on:
+ *   PLAIN   f_j = base^(-2 j / rot)
+ *   LINEAR  f_j / factor: positions closer together
+ *   BASE    base * factor^(rot / (rot - 2)) as the base: the slowest pair as
+ *           with LINEAR, the fastest as it is
+ *   PARTS   by the turns r_j = original_positions * f_j / (2 pi) that a pair
+ *           makes: f_j / factor up to low_turns, f_j from high_turns on,
+ *           (1 - t) f_j / factor + t f_j with t = (r_j - low_turns) /
+ *           (high_turns - low_turns) between them */
+typedef enum { TQ_ROTARY_PLAIN = 0, TQ_ROTARY_LINEAR = 1, TQ_ROTARY_BASE = 2, TQ_ROTARY_PARTS = 3 } tq_rotary_scaling;
+
+/* Host only: the rot / 2 frequencies (radians a position), in out.  Arguments
+ * that the scaling does not name are not looked at. */
+TQ_API tq_status tq_rotary_frequencies(int rot, double base, tq_rotary_scaling scaling, double factor, double original_positions,
+                                       double low_turns, double high_turns, double* out);
+
+/* Fill a table for positions 0 .. num_positions - 1, computed in 64 bits and
+ * rounded once.  frequencies: host, rot / 2 finite values, read before the
+ * call returns; magnitude: positive and finite. */
+TQ_API tq_status tq_rotary_table(const double* frequencies, int rot, double magnitude, int64_t num_positions, float* table,
+                                 void* stream);
+
+/* Rotate num_tokens rows of [num_heads, d] of `dtype`, token t by position
+ * positions[t] (device int32): x and out strided like K of tq_fp8_write, with
+ * d any multiple of 16 (at most 4096), rot <= d.  out may be x with the same
+ * strides (in place, where the dims from rot on are not touched); apart from
+ * that its rows overlap neither each other nor the memory from x's first to
+ * its last row.  transpose != 0 rotates by the transposed matrix: for an
+ * output's gradient it gives the input's (and for m = 1 it undoes the
+ * rotation).  Computed in fp32, every product and sum rounded, and rounded to
+ * the type once.  A position outside the table sets TQ_FLAG_BAD_SLOT and leaves
+ * the token's output rows as they were. */
+TQ_API tq_status tq_rotary(const void* x, tq_dtype dtype, int64_t x_token_stride, int64_t x_head_stride, int64_t num_tokens,
+                           int num_heads, int d, const int32_t* positions, const float* table, int64_t num_positions, int rot,
+                           tq_rotary_layout layout, int transpose, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                           int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Drafted tokens over the 8-bit cache                                     */
+/* ---------------------------------------------------------------------- */
+
+/* tq_fp8_write with the keys rotated on the way, and the step's queries with
+ * them in the same launch.  A packed row's position is positions[row] (device
+ * int32 [num_tokens]) or, with positions NULL, where it is written (start[b] +
+ * its place in the sequence); the two differ for a tree of drafts, whose nodes
+ * have consecutive slots and their depths as positions.  Rotated keys are
+ * rounded to e4m3 from fp32 and enter the block's maximum as such; V is written
+ * as tq_fp8_write does.  A position outside the table sets TQ_FLAG_BAD_SLOT:
+ * its key is stored as zeros, its query's output rows are left as they were.
+ * q: device, num_tokens rows of [num_q_heads, 128] of `dtype`, or NULL; q_out
+ * as out of tq_rotary (q_out = q allowed), apart from K and V; its rows that
+ * belong to no sequence are left as they were.  rot <= 128. */
+TQ_API tq_status tq_fp8_append(const tq_fp8_cache* cache, const void* K, const void* V, tq_dtype dtype, int64_t k_token_stride,
+                               int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                               int64_t q_token_stride, int64_t q_head_stride, int num_q_heads, void* q_out,
+                               int64_t out_token_stride, int64_t out_head_stride, int64_t num_tokens, int batch,
+                               const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table, int max_blocks_per_seq,
+                               const int32_t* positions, const float* table, int64_t num_positions, int rot,
+                               tq_rotary_layout layout, int32_t* dev_status, void* stream);
+
+/* Attention of a ragged batch of trees of drafted tokens, whose keys and
+ * values are in the cache already: sequence b's n = cu_tokens[b + 1] -
+ * cu_tokens[b] rows are nodes 0 .. n - 1 at positions start[b] + node.  A node
+ * attends over every position before start[b] and over the nodes j of its own
+ * sequence whose bit is set in its row of the mask (device uint64
+ * [num_tokens, mask_words], 8-byte aligned; bit j % 64 of word j / 64): itself
+ * only if its own bit is set, none from 64 * mask_words on, and bits from n on
+ * do not count.  A row that attends to nothing is zero.  Everything else is as
+ * for tq_fp8_prefill_attention, the precision and the workspace's rules too. */
+TQ_API size_t tq_fp8_tree_workspace_bytes(const tq_fp8_cache* cache, int64_t num_tokens, int batch, int num_q_heads);
+TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_token_stride,
+                                       int64_t q_head_stride, int64_t num_tokens, int batch, int num_q_heads,
+                                       const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table,
+                                       int max_blocks_per_seq, const uint64_t* mask, int mask_words, float sm_scale, void* out,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Keep the accepted nodes of every tree: with kept rows r = 0 .. n - 1 of
+ * sequence b (kept[cu_kept[b] + r], device int32 [num_kept], increasing, so
+ * that kept[r] >= r; cu_kept like cu_tokens), position start[b] + r becomes what
+ * position start[b] + kept[r] was, keys and values of every head.  The next
+ * step's start is start[b] + n.  A block that receives rows takes the largest
+ * scale of the blocks they come from and, where it holds earlier positions of
+ * the sequence (start[b] inside the block), of its own; codes move to it as in
+ * tq_fp8_write, which is exact but for those that become subnormal.  Slots behind
+ * the last kept row keep their bytes, and sequences without kept rows
+ * everything.  A negative kept row or one below its place, a block id outside
+ * the pool, a position past the block table and a negative start set
+ * TQ_FLAG_BAD_SLOT; those rows are skipped. */
+TQ_API tq_status tq_fp8_keep(const tq_fp8_cache* cache, int64_t num_kept, int batch, const int32_t* cu_kept, const int32_t* kept,
+                             const int32_t* start, const int32_t* block_table, int max_blocks_per_seq, int32_t* dev_status,
+                             void* stream);
+
 /* Whether code on the current device can read and write the memory at p:
  * memory of this device, managed memory, or page-locked host memory mapped
  * into the device's address space at the same address (under unified

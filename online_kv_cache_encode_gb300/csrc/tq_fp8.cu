@@ -16,143 +16,10 @@
 // x 256 x (1 + element size) bytes is what they cannot do without.
 #include <cuda_runtime.h>
 
-#include "tq_fp8.cuh"
+#include "tq_fp8_rows.cuh"
 
 namespace tq {
 namespace {
-
-constexpr int kWarps = 8;
-constexpr int kRows = 16;  // tokens a warp holds
-
-// Where one warp works: 16 positions of a block.
-struct Place {
-    bool live;       // the unit has tokens there
-    int blk;         // the block's id, not checked yet (-1: past the block table)
-    int64_t row0;    // packed row of the warp's first token (may lie before the sequence's first)
-    int first;       // offset of the warp's 16 tokens in the block
-    int lo, hi;      // offsets in the block of the new tokens: lo <= t < hi
-    int head, side;
-};
-
-// Work item `w` (16 tokens) of the launch; 2^wpb_shift warps per block of tokens.
-__device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch& b, int64_t w, int wpb_shift,
-                                            int32_t* status) {
-    Place p;
-    const int64_t item = w >> wpb_shift;
-    p.first = (int)(w & ((1 << wpb_shift) - 1)) * kRows;
-    p.side = (int)(item & 1);
-    const uint32_t uh = (uint32_t)(item >> 1);  // the host keeps the grid, and so this, below 2^31
-    const uint32_t u = uh / (uint32_t)g.hkv;
-    p.head = (int)(uh - u * (uint32_t)g.hkv);
-    p.live = false;
-    p.blk = -1;
-    p.row0 = 0;
-    p.lo = p.hi = 0;
-    if (u >= fp8_units(b.num_tokens, b.batch, g.bs, 2)) return p;
-    const Fp8Seq q = fp8_seq_of_unit(b, u, g.bs, 2);
-    const int s = q.b, c0 = q.row0, n = q.n, start = q.start;
-    const int64_t j = (int64_t)u - q.base;
-    if (n <= 0 || j < 0) return p;
-    if (start < 0) {
-        if (j == 0 && (threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
-        return p;
-    }
-    const int64_t blk_i = (start >> g.bs_shift) + j;  // the block of the sequence
-    const int64_t pos0 = blk_i << g.bs_shift;
-    if (pos0 >= (int64_t)start + n) return p;
-    if (blk_i < b.max_blocks) p.blk = __ldg(b.block_table + (int64_t)s * b.max_blocks + blk_i);
-    p.live = true;
-    p.row0 = (int64_t)c0 + (pos0 - start) + p.first;
-    p.lo = start > pos0 ? (int)(start - pos0) : 0;
-    p.hi = (int)min((int64_t)g.bs, (int64_t)start + n - pos0);
-    return p;
-}
-// Whether the place's block lies in the pool (else it is flagged); its page is (blk * hkv + head) * 2 + side.
-__device__ __forceinline__ bool page_of(const Fp8Geometry& g, const Place& p, int32_t* status, int64_t& page) {
-    if (p.blk < 0 || p.blk >= g.num_blocks) {
-        if (p.live && (threadIdx.x & 31) == 0) flag(status, TQ_FLAG_BAD_SLOT);
-        return false;
-    }
-    page = ((int64_t)p.blk * g.hkv + p.head) * 2 + p.side;
-    return true;
-}
-
-// A 16-byte piece of a row: V elements.  top() is the largest magnitude as an
-// integer (magnitudes order as their bits do, infinities and NaN above all).
-template <typename T>
-struct Elem;
-template <>
-struct Elem<float> {
-    static constexpr int V = 4;
-    static constexpr uint32_t kInf = 0x7F800000u;
-    static __device__ __forceinline__ uint32_t top(const uint4& r, uint32_t m) {
-        return max(max(m, max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu)), max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
-    }
-    static __device__ __forceinline__ uint32_t join(uint32_t m) { return m; }
-    static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m); }
-    static __device__ __forceinline__ void get(const uint4& r, float (&x)[4]) {
-        x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-    }
-    static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    }
-};
-// Two 16-bit elements in a word: magnitudes and maxima two at a time.
-struct Elem16 {
-    static constexpr int V = 8;
-    static __device__ __forceinline__ uint32_t top(const uint4& r, uint32_t m) {
-        const uint32_t a = __vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), b = __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu);
-        return __vmaxu2(m, __vmaxu2(a, b));
-    }
-    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
-};
-template <>
-struct Elem<__nv_bfloat16> : Elem16 {
-    static constexpr uint32_t kInf = 0x7F80u;
-    static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m << 16); }
-    static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-    static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <>
-struct Elem<__half> : Elem16 {
-    static constexpr uint32_t kInf = 0x7C00u;
-    static __device__ __forceinline__ float value(uint32_t m) { return __half2float(__ushort_as_half((unsigned short)m)); }
-    static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
-    static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // A lane holds 16-byte pieces: LPR lanes make a row of 128 elements, a warp
 // RPI rows at a time.
@@ -230,16 +97,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 2 : 5) fp8_write
             else *reinterpret_cast<uint32_t*>(dst + r * kHeadDim) = w[0];
         }
     }
-    if (p.lo > p.first && e > e_old) {  // earlier rows move to the larger scale
-        const float m = fp8_pow2(max(e_old - e, -100));
-        for (int r = 0; r < min(p.lo - p.first, kRows); ++r) {
-            uint32_t* c = reinterpret_cast<uint32_t*>(a.g.pool + page * ((int64_t)a.g.bs * kHeadDim) +
-                                                      (int64_t)(p.first + r) * kHeadDim) + lane;
-            const uint32_t v = *c;
-            const float2 x = fp8_to_float2(v & 0xFFFFu), y = fp8_to_float2(v >> 16);
-            *c = fp8_cvt2(x.x * m, x.y * m) | (fp8_cvt2(y.x * m, y.y * m) << 16);
-        }
-    }
+    if (p.lo > p.first && e > e_old)  // earlier rows move to the larger scale
+        move_codes(a.g.pool + page * ((int64_t)a.g.bs * kHeadDim) + (int64_t)p.first * kHeadDim, min(p.lo - p.first, kRows), e_old - e);
 }
 
 template <typename T>
@@ -282,19 +141,14 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_read_kernel(const Fp8ReadArgs
     }
 }
 
-int64_t grid_of(const Fp8Geometry& g, const Fp8Batch& b) {
-    const int64_t warps = (fp8_units(b.num_tokens, b.batch, g.bs, 2) * g.hkv * 2) << (g.bs_shift - 4);
-    return (warps + kWarps - 1) / kWarps;
-}
-
 }  // namespace
 
-bool fp8_rows_count(const Fp8Geometry& g, const Fp8Batch& b) { return grid_of(g, b) < (1 << 28); }
+bool fp8_rows_count(const Fp8Geometry& g, const Fp8Batch& b) { return fp8_row_grid(g, b) < (1 << 28); }
 
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int shift = a.g.bs_shift - 4;
-    const dim3 grid((unsigned)grid_of(a.g, a.b)), block(kWarps * 32);
+    const dim3 grid((unsigned)fp8_row_grid(a.g, a.b)), block(kWarps * 32);
     if (a.dtype == TQ_F32) return (int)launch_programmatic(fp8_write_kernel<float>, grid, block, 0, s, a, shift);
     if (a.dtype == TQ_BF16) return (int)launch_programmatic(fp8_write_kernel<__nv_bfloat16>, grid, block, 0, s, a, shift);
     return (int)launch_programmatic(fp8_write_kernel<__half>, grid, block, 0, s, a, shift);
@@ -303,7 +157,7 @@ int launch_fp8_write(const Fp8WriteArgs& a, void* stream) {
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int shift = a.g.bs_shift - 4;
-    const dim3 grid((unsigned)grid_of(a.g, a.b)), block(kWarps * 32);
+    const dim3 grid((unsigned)fp8_row_grid(a.g, a.b)), block(kWarps * 32);
     if (a.dtype == TQ_F32) return (int)launch_programmatic(fp8_read_kernel<float>, grid, block, 0, s, a, shift);
     if (a.dtype == TQ_BF16) return (int)launch_programmatic(fp8_read_kernel<__nv_bfloat16>, grid, block, 0, s, a, shift);
     return (int)launch_programmatic(fp8_read_kernel<__half>, grid, block, 0, s, a, shift);

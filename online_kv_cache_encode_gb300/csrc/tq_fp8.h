@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "tq_internal.h"
+#include "tq_rotary.h"
 
 namespace tq {
 
@@ -52,6 +53,26 @@ struct Fp8ReadArgs {
     int dtype;
     int32_t* status;
 };
+struct Fp8AppendArgs {
+    Fp8Geometry g;
+    Fp8Batch b;
+    const void* K;
+    const void* V;
+    const void* q;  // null: no queries
+    void* q_out;
+    int dtype;
+    int64_t k_token, k_head, v_token, v_head, q_token, q_head, out_token, out_head;  // strides in elements
+    int hq;
+    RotaryTable r;
+    const int32_t* positions;  // of every packed row; null: start + its place in the sequence
+    int32_t* status;
+};
+struct Fp8KeepArgs {
+    Fp8Geometry g;
+    Fp8Batch b;            // of the kept rows
+    const int32_t* kept;   // row r of a sequence is what was at position start + kept[r]
+    int32_t* status;
+};
 struct Fp8AttnArgs {
     Fp8Geometry g;
     Fp8Batch b;
@@ -60,6 +81,8 @@ struct Fp8AttnArgs {
     int dtype;
     int64_t q_token, q_head;  // strides in elements
     int hq, group;
+    const uint64_t* mask;  // trees: of every packed row `words` words, bit j: it sees row j of its sequence
+    int words;
     float sm_scale_log2;
     void* out;  // [rows][hq][128], q's type
     int32_t* status;
@@ -68,6 +91,10 @@ struct Fp8AttnArgs {
 bool fp8_rows_count(const Fp8Geometry& g, const Fp8Batch& b);  // work items are counted in 32 bits
 int launch_fp8_write(const Fp8WriteArgs& a, void* stream);
 int launch_fp8_read(const Fp8ReadArgs& a, void* stream);
+bool fp8_append_counts(const Fp8Geometry& g, const Fp8Batch& b, int hq);
+int launch_fp8_append(const Fp8AppendArgs& a, void* stream);
+bool fp8_keep_counts(const Fp8Geometry& g, int batch);
+int launch_fp8_keep(const Fp8KeepArgs& a, void* stream);
 // The pool as rows of 128 codes: the tensor map whose boxes have `rows` of them.
 bool fp8_tensor_map(CUtensorMap* map, const Fp8Geometry& g, int rows);
 bool fp8_decode_counts(const Fp8Geometry& g, int batch, int group, int max_blocks);  // tiles are counted in 32 bits

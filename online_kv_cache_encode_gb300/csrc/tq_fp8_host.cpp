@@ -197,6 +197,79 @@ TQ_API tq_status tq_fp8_read(const tq_fp8_cache* c, void* K, void* V, tq_dtype d
     return e ? cuda_fail((cudaError_t)e, "read launch") : TQ_OK;
 }
 
+TQ_API tq_status tq_fp8_append(const tq_fp8_cache* c, const void* K, const void* V, tq_dtype dtype, int64_t k_token_stride,
+                               int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                               int64_t q_token_stride, int64_t q_head_stride, int num_q_heads, void* q_out,
+                               int64_t out_token_stride, int64_t out_head_stride, int64_t num_tokens, int batch,
+                               const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table, int max_blocks_per_seq,
+                               const int32_t* positions, const float* table, int64_t num_positions, int rot,
+                               tq_rotary_layout layout, int32_t* dev_status, void* stream) {
+    tq_status st = check_batch(c, num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    if (st != TQ_OK) return st;
+    bool unsupported;
+    const char* fault = rotary_table_fault(table, num_positions, rot, (int)layout, &unsupported);
+    if (fault) return fail(unsupported ? TQ_ERR_UNSUPPORTED : TQ_ERR_INVALID_ARG, fault);
+    if (rot > kHeadDim) return fail(TQ_ERR_INVALID_ARG, "more rotated dims than a head has");
+    if (!known(dtype)) return fail(TQ_ERR_INVALID_ARG, "bad dtype");
+    if (num_tokens == 0 || batch == 0) return TQ_OK;
+    if (!K || !V) return fail(TQ_ERR_INVALID_ARG, "K and V must be non-NULL");
+    const int64_t elem = dtype == TQ_F32 ? 4 : 2;
+    if (bad_rows(K, k_token_stride, k_head_stride, elem) || bad_rows(V, v_token_stride, v_head_stride, elem))
+        return fail(TQ_ERR_INVALID_ARG, "the rows of K and V must be 16-byte aligned");
+    if (q) {
+        if (num_q_heads <= 0 || !q_out) return fail(TQ_ERR_INVALID_ARG, "queries need num_q_heads and q_out");
+        if (bad_rows(q, q_token_stride, q_head_stride, elem) || bad_rows(q_out, out_token_stride, out_head_stride, elem))
+            return fail(TQ_ERR_INVALID_ARG, "the rows of q and q_out must be 16-byte aligned");
+        if (const char* f = rotary_rows_fault(q, q_token_stride, q_head_stride, q_out, out_token_stride, out_head_stride, num_tokens,
+                                              num_q_heads, kHeadDim, (int)elem))
+            return fail(TQ_ERR_INVALID_ARG, f);
+    }
+    Fp8AppendArgs a{};
+    a.g = c->g;
+    a.b = make_batch(num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    if (!fp8_append_counts(a.g, a.b, q ? num_q_heads : 0)) return fail(TQ_ERR_UNSUPPORTED, "more rows than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
+    a.K = K;
+    a.V = V;
+    a.q = q;
+    a.q_out = q_out;
+    a.dtype = (int)dtype;
+    a.k_token = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_token = v_token_stride;
+    a.v_head = v_head_stride;
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.hq = q ? num_q_heads : 0;
+    a.r.table = table;
+    a.r.positions = num_positions;
+    a.r.rot = rot;
+    a.r.interleaved = layout == TQ_ROTARY_INTERLEAVED;
+    a.positions = positions;
+    a.status = dev_status;
+    const int e = launch_fp8_append(a, stream);
+    return e ? cuda_fail((cudaError_t)e, "append launch") : TQ_OK;
+}
+
+TQ_API tq_status tq_fp8_keep(const tq_fp8_cache* c, int64_t num_kept, int batch, const int32_t* cu_kept, const int32_t* kept,
+                             const int32_t* start, const int32_t* block_table, int max_blocks_per_seq, int32_t* dev_status,
+                             void* stream) {
+    tq_status st = check_batch(c, num_kept, batch, cu_kept, start, block_table, max_blocks_per_seq);
+    if (st != TQ_OK || num_kept == 0 || batch == 0) return st;
+    if (!kept) return fail(TQ_ERR_INVALID_ARG, "kept must be non-NULL");
+    if (!fp8_keep_counts(c->g, batch)) return fail(TQ_ERR_UNSUPPORTED, "more sequences than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
+    Fp8KeepArgs a{};
+    a.g = c->g;
+    a.b = make_batch(num_kept, batch, cu_kept, start, block_table, max_blocks_per_seq);
+    a.kept = kept;
+    a.status = dev_status;
+    const int e = launch_fp8_keep(a, stream);
+    return e ? cuda_fail((cudaError_t)e, "keep launch") : TQ_OK;
+}
+
 TQ_API size_t tq_fp8_decode_workspace_bytes(const tq_fp8_cache* c, int batch, int num_q_heads) {
     if (!c || batch <= 0 || num_q_heads <= 0 || num_q_heads % c->g.hkv) return 0;
     return fp8_decode_workspace(c->g, batch, num_q_heads / c->g.hkv);
@@ -269,6 +342,43 @@ TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* c, const void* q, 
     a.status = dev_status;
     const int e = launch_fp8_prefill(a, c->side, workspace, stream);
     return e ? cuda_fail((cudaError_t)e, "prefill launch") : TQ_OK;
+}
+
+TQ_API size_t tq_fp8_tree_workspace_bytes(const tq_fp8_cache* c, int64_t num_tokens, int batch, int num_q_heads) {
+    return tq_fp8_prefill_workspace_bytes(c, num_tokens, batch, num_q_heads);
+}
+
+TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64_t q_token_stride,
+                                       int64_t q_head_stride, int64_t num_tokens, int batch, int num_q_heads,
+                                       const int32_t* cu_tokens, const int32_t* start, const int32_t* block_table,
+                                       int max_blocks_per_seq, const uint64_t* mask, int mask_words, float sm_scale, void* out,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    tq_status st = check_batch(c, num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    if (st != TQ_OK || num_tokens == 0 || batch == 0) return st;
+    st = check_attn(c, q, dtype, q_token_stride, q_head_stride, num_q_heads, sm_scale, out, workspace, workspace_bytes,
+                    tq_fp8_tree_workspace_bytes(c, num_tokens, batch, num_q_heads));
+    if (st != TQ_OK) return st;
+    if (!mask || misaligned(mask, 8)) return fail(TQ_ERR_INVALID_ARG, "mask must be non-NULL and 8-byte aligned");
+    if (mask_words <= 0) return fail(TQ_ERR_INVALID_ARG, "mask_words must be positive");
+    if (!fp8_prefill_counts(c->g, num_tokens, batch, num_q_heads / c->g.hkv))
+        return fail(TQ_ERR_UNSUPPORTED, "more query rows than a launch holds");
+    if ((st = check_device(c)) != TQ_OK) return st;
+    Fp8AttnArgs a{};
+    a.g = c->g;
+    a.b = make_batch(num_tokens, batch, cu_tokens, start, block_table, max_blocks_per_seq);
+    a.q = q;
+    a.dtype = (int)dtype;
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.hq = num_q_heads;
+    a.group = num_q_heads / c->g.hkv;
+    a.mask = mask;
+    a.words = mask_words;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.out = out;
+    a.status = dev_status;
+    const int e = launch_fp8_prefill(a, c->side, workspace, stream);
+    return e ? cuda_fail((cudaError_t)e, "tree attention launch") : TQ_OK;
 }
 
 }  // extern "C"

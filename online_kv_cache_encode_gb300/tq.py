@@ -23,8 +23,8 @@ TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 NOALLOC_WORKSPACE_BYTES = 4 << 20  # TQ_NOALLOC_WORKSPACE_BYTES
 
 # every exported symbol of include/tq.h: (restype, argtypes)
-_P, _I, _I64, _U64, _F, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
-                               ctypes.c_float, ctypes.c_size_t)
+_P, _I, _I64, _U64, _F, _SZ, _D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
+                                   ctypes.c_float, ctypes.c_size_t, ctypes.c_double)
 SIGNATURES = {
     "tq_codebook_init": (_I, [_I, _I, ctypes.POINTER(_P)]),
     "tq_codebook_get": (_I, [_P, _P, _P, _P]),
@@ -56,6 +56,14 @@ SIGNATURES = {
     "tq_fp8_decode_attention": (_I, [_P, _P, _I, _I64, _I64, _I, _I, _P, _I, _P, _F, _P, _P, _SZ, _P, _P]),
     "tq_fp8_prefill_workspace_bytes": (_SZ, [_P, _I64, _I, _I]),
     "tq_fp8_prefill_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _P, _I, _F, _P, _P, _SZ, _P, _P]),
+    "tq_rotary_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, _P]),
+    "tq_rotary_table": (_I, [_P, _I, _D, _I64, _P, _P]),
+    "tq_rotary": (_I, [_P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _I64, _I, _I, _I, _P, _I64, _I64, _P, _P]),
+    "tq_fp8_append": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I, _P, _I64, _I64, _I64, _I, _P, _P, _P, _I,
+                           _P, _P, _I64, _I, _I, _P, _P]),
+    "tq_fp8_tree_workspace_bytes": (_SZ, [_P, _I64, _I, _I]),
+    "tq_fp8_tree_attention": (_I, [_P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _P, _I, _P, _I, _F, _P, _P, _SZ, _P, _P]),
+    "tq_fp8_keep": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I, _P, _P]),
     "tq_device_accessible": (_I, [_P, ctypes.POINTER(_I)]),
     "tq_test_stall_waits": (None, [_I64]),
     "tq_selftest_tcgen05": (_I, [_P, _P, _P, _P, _P]),
@@ -383,6 +391,83 @@ def octopus_codebook(d: int, bits: int, kind: int) -> np.ndarray:
     return out
 
 
+_ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROTARY_SCALINGS = {None: (0, 0), "linear": (1, 1), "base": (2, 1), "parts": (3, 4)}  # code, arguments
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: tuple | None = None) -> np.ndarray:
+    """The dim / 2 frequencies (radians a position, float64) of rotated pairs.  scaling: None, ("linear", factor),
+    ("base", factor) or ("parts", factor, original_positions, low_turns, high_turns), as tq_rotary_frequencies has them."""
+    kind, *args = scaling or (None,)
+    if kind not in _ROTARY_SCALINGS or len(args) != _ROTARY_SCALINGS[kind][1]:
+        raise TQError(TQ_ERR_INVALID_ARG, f"bad rotary scaling {scaling!r}")
+    factor, original, low, high = (*map(float, args), *(0.0,) * (4 - len(args)))
+    out = np.empty(max(dim, 2) // 2, dtype=np.float64)
+    _check(lib().tq_rotary_frequencies(dim, base, _ROTARY_SCALINGS[kind][0], factor, original, low, high,
+                                       out.ctypes.data_as(ctypes.c_void_p)))
+    return out
+
+
+class Rotary:
+    """Rotary positions 0 .. num_positions - 1 for the first `dim` dims of a head (a multiple of 16, at most 256).
+
+    layout: "half" (dim j pairs with j + dim / 2) or "interleaved" (2 j with 2 j + 1); base and scaling as
+    rotary_frequencies has them, or the frequencies themselves; magnitude multiplies what is rotated.  The cosines and
+    sines are computed once, here, into `table` (fp32 [num_positions, 2, dim / 2]) on the current stream, unless a
+    table is given.
+    """
+
+    def __init__(self, dim: int, num_positions: int, base: float = 10000.0, layout: str = "half",
+                 scaling: tuple | None = None, frequencies=None, magnitude: float = 1.0,
+                 table: torch.Tensor | None = None, device="cuda"):
+        if layout not in _ROTARY_LAYOUTS:
+            raise TQError(TQ_ERR_INVALID_ARG, f"bad rotary layout {layout!r}")
+        if dim <= 0 or dim % 16 or dim > 256 or num_positions <= 0:
+            raise TQError(TQ_ERR_UNSUPPORTED, "the rotated dims must be a multiple of 16, at most 256")
+        self.dim, self.num_positions, self.layout = dim, num_positions, layout
+        self._layout, self._lib = _ROTARY_LAYOUTS[layout], lib()
+        if table is None:
+            if frequencies is None:
+                frequencies = rotary_frequencies(dim, base, scaling)
+            f = np.ascontiguousarray(frequencies, dtype=np.float64)
+            assert f.shape == (dim // 2,)
+            table = torch.empty((num_positions, 2, dim // 2), dtype=torch.float32, device=device)
+            with torch.cuda.device(table.device):
+                _check(self._lib.tq_rotary_table(f.ctypes.data_as(ctypes.c_void_p), dim, float(magnitude), num_positions,
+                                                 table.data_ptr(), _stream()))
+        assert table.is_cuda and table.dtype is torch.float32 and table.shape == (num_positions, 2, dim // 2)
+        assert table.is_contiguous()
+        self.table, self._dev = table, table.get_device()
+
+    def apply(self, x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor | None = None, transpose: bool = False,
+              status: torch.Tensor | None = None) -> torch.Tensor:
+        """x: [T, H, d] (f32/bf16/f16, strided rows on 16-byte boundaries, d a multiple of 16), token t rotated by
+        position positions[t] (int32 [T], on the device) -> out, a new contiguous tensor unless given (x itself: in
+        place).  transpose: by the transposed matrix, which takes an output's gradient to the input's.  The call records
+        no gradient itself."""
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.apply(x, positions, out, transpose, status)
+        dev = self._dev
+        T, H, d = x.shape
+        if out is None:
+            out = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
+        else:
+            assert out.shape == x.shape and out.dtype is x.dtype and out.get_device() == dev
+        xs, os = x.stride(), out.stride()
+        assert x.get_device() == dev and (d == 1 or xs[2] == 1 and os[2] == 1)
+        assert positions.dtype is torch.int32 and positions.get_device() == dev and positions.is_contiguous()
+        assert positions.numel() == T
+        assert status is None or status.dtype is torch.int32 and status.get_device() == dev and status.numel() >= 1
+        st = self._lib.tq_rotary(x.data_ptr(), _DTYPE_CODES[x.dtype], xs[0] if T > 1 else 0, xs[1] if H > 1 else 0, T, H, d,
+                                 positions.data_ptr(), self.table.data_ptr(), self.num_positions, self.dim, self._layout,
+                                 int(transpose), out.data_ptr(), os[0] if T > 1 else 0, os[1] if H > 1 else 0, _ptr(status),
+                                 torch._C._cuda_getCurrentRawStream(dev))
+        if st:
+            _check(st)
+        return out
+
+
 class Fp8Cache:
     """An 8-bit paged KV cache on the current CUDA device: e4m3 codes and one
     power-of-two scale for each block, KV head and side (tq_fp8_cache_create).
@@ -569,3 +654,79 @@ class Fp8Cache:
         if st:
             _check(st)
         return out
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
+               block_table: torch.Tensor, rotary: Rotary, positions: torch.Tensor | None = None,
+               q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, status: torch.Tensor | None = None):
+        """write(), with the keys rotated on the way by their positions: int32 [T], or where they are written.  With q
+        ([T, Hq, d] of K's type) its rows are rotated by the same launch -> q_out, a new contiguous tensor unless given
+        (q itself: in place); rows that belong to no sequence are not written.  Without q -> None."""
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.append(K, V, cu_tokens, start, block_table, rotary, positions, q, q_out, status)
+        B, mb = self._batch(cu_tokens, start, block_table, status)
+        ks, vs = self._rows(K, self.hkv), self._rows(V, self.hkv)
+        T, dtype = K.shape[0], K.dtype
+        assert V.shape[0] == T and V.dtype is dtype and rotary._dev == self._dev
+        if positions is not None:
+            assert positions.dtype is torch.int32 and positions.get_device() == self._dev and positions.is_contiguous()
+            assert positions.numel() == T
+        qs, os, hq = (0, 0), (0, 0), 0
+        if q is not None:
+            hq = q.shape[1]
+            qs = self._rows(q, hq)
+            assert q.shape[0] == T and q.dtype is dtype
+            if q_out is None:
+                q_out = torch.empty((T, hq, self.d), dtype=dtype, device=q.device)
+            assert q_out.shape == q.shape and q_out.dtype is dtype
+            os = self._rows(q_out, hq)
+        else:
+            assert q_out is None
+        st = self._lib.tq_fp8_append(self._h, K.data_ptr(), V.data_ptr(), _DTYPE_CODES[dtype], *ks, *vs, _ptr(q), *qs, hq,
+                                     _ptr(q_out), *os, T, B, cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(),
+                                     mb, _ptr(positions), rotary.table.data_ptr(), rotary.num_positions, rotary.dim,
+                                     rotary._layout, _ptr(status), torch._C._cuda_getCurrentRawStream(self._dev))
+        if st:
+            _check(st)
+        return q_out
+
+    def tree(self, q: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor,
+             mask: torch.Tensor, sm_scale: float | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+        """Attention of a ragged batch of trees of drafted tokens (q: [T, Hq, d]; their keys and values written before):
+        node i of a sequence sees every position before start[b] and the nodes j with bit j % 64 of word j / 64 set in
+        its row of mask (int64 [T, words], contiguous) -> out [T, Hq, d] of q's type.  Rows that belong to no sequence
+        are not written."""
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.tree(q, cu_tokens, start, block_table, mask, sm_scale, out, workspace, status)
+        B, mb = self._batch(cu_tokens, start, block_table, status)
+        T, hq, strides, sm_scale, out = self._attend_args(q, sm_scale, out)
+        rows, words = mask.shape
+        assert rows == T and mask.dtype is torch.int64 and mask.get_device() == self._dev and mask.is_contiguous()
+        stream = torch._C._cuda_getCurrentRawStream(self._dev)
+        if workspace is None:
+            workspace = self._workspace("tree", (T, B, hq), stream, self._lib.tq_fp8_tree_workspace_bytes)
+        else:
+            assert workspace.get_device() == self._dev and workspace.is_contiguous()
+        st = self._lib.tq_fp8_tree_attention(self._h, q.data_ptr(), _DTYPE_CODES[q.dtype], *strides, T, B, hq,
+                                             cu_tokens.data_ptr(), start.data_ptr(), block_table.data_ptr(), mb,
+                                             mask.data_ptr(), words, sm_scale, out.data_ptr(), workspace.data_ptr(),
+                                             workspace.nbytes, _ptr(status), stream)
+        if st:
+            _check(st)
+        return out
+
+    def keep(self, cu_kept: torch.Tensor, kept: torch.Tensor, start: torch.Tensor, block_table: torch.Tensor,
+             status: torch.Tensor | None = None) -> None:
+        """Moves the accepted nodes up: position start[b] + r becomes what position start[b] + kept[cu_kept[b] + r] was
+        (kept: int32, increasing in every sequence; cu_kept: int32 [B + 1])."""
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.keep(cu_kept, kept, start, block_table, status)
+        B, mb = self._batch(cu_kept, start, block_table, status)
+        assert kept.dtype is torch.int32 and kept.get_device() == self._dev and kept.is_contiguous()
+        st = self._lib.tq_fp8_keep(self._h, kept.numel(), B, cu_kept.data_ptr(), kept.data_ptr(), start.data_ptr(),
+                                   block_table.data_ptr(), mb, _ptr(status), torch._C._cuda_getCurrentRawStream(self._dev))
+        if st:
+            _check(st)
