@@ -4,10 +4,15 @@
 //
 // A block that receives codes takes the largest exponent of the blocks they come
 // from and, where it holds earlier positions of the sequence, of its own; codes move by
-// c -> c 2^(e_from - e), which is exact but for those that become subnormal.  With
-// r <= kept[r] a position's codes are read before, or at the same time as, anything is
-// written over them, if the rows go in order: one warp takes a (sequence, head, side)
-// and goes through its rows in order, those of a block with the block's final exponent.
+// c -> c 2^(e_from - e), which is exact but for those that become subnormal.
+//
+// With r <= kept[r], nothing that is written lies in front of what is still to be read, if
+// the rows go in order.  So one CTA takes a (sequence, head, side) and goes through the
+// places 128 at a time, which is a whole number of blocks: every row of the 128 is in
+// registers, and every exponent known, before any of them is written.  A warp has 16
+// places; a lane looks one of them up, so that the chain of loads (kept row, block id,
+// scale, codes) is paid once for all of them.  Earlier positions of the first block are
+// rows that come from where they are.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -17,95 +22,91 @@
 namespace tq {
 namespace {
 
-constexpr int kBatch = 16;  // rows that a warp has in flight
+constexpr int kPlaces = kWarps * kRows;  // of a CTA's step
 
 __global__ void __launch_bounds__(kWarps * 32) fp8_keep_kernel(const Fp8KeepArgs a) {
     const Fp8Geometry& g = a.g;
-    const int lane = threadIdx.x & 31;
+    __shared__ int tops[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t hs = item >> 1;
-    const int side = (int)(item & 1), b = (int)(hs / g.hkv), h = (int)(hs - (int64_t)b * g.hkv);
-    if (b >= a.b.batch) return;
+    const int64_t hs = blockIdx.x >> 1;
+    const int side = (int)(blockIdx.x & 1), b = (int)(hs / g.hkv), h = (int)(hs - (int64_t)b * g.hkv);
     const int c0 = fp8_clamp_cu(a.b.cu, b, a.b.num_tokens), n = fp8_clamp_cu(a.b.cu, b + 1, a.b.num_tokens) - c0;
     const int start = __ldg(a.b.start + b);
     if (n <= 0) return;
     if (start < 0) {
-        if (lane == 0) flag(a.status, TQ_FLAG_BAD_SLOT);
+        if (threadIdx.x == 0) flag(a.status, TQ_FLAG_BAD_SLOT);
         return;
     }
-    const int32_t* row = a.b.block_table + (int64_t)b * a.b.max_blocks;
+    const int32_t* table = a.b.block_table + (int64_t)b * a.b.max_blocks;
     // the page that holds a position of the sequence, or -1
     auto page_of_pos = [&](int64_t p) -> int64_t {
         const int64_t j = p >> g.bs_shift;
-        const int id = j < a.b.max_blocks ? __ldg(row + j) : -1;
+        const int id = j < a.b.max_blocks ? __ldg(table + j) : -1;
         return id >= 0 && id < g.num_blocks ? ((int64_t)id * g.hkv + h) * 2 + side : -1;
     };
-    // where row r comes from: its page (-1: it is skipped) and slot
-    auto source = [&](int r, int& slot) -> int64_t {
-        const int k = __ldg(a.kept + c0 + r);
-        const int64_t p = (int64_t)start + k;
-        slot = (int)(p & (g.bs - 1));
-        return k >= r ? page_of_pos(p) : -1;
-    };
-    const int64_t stride = (int64_t)g.bs * kHeadDim;
-    for (int r0 = 0; r0 < n;) {  // block by block
-        const int64_t p0 = (int64_t)start + r0;
-        const int off = (int)(p0 & (g.bs - 1)), m = min(g.bs - off, n - r0);
-        const int64_t page = page_of_pos(p0);
+    const int64_t first = (int64_t)start >> g.bs_shift << g.bs_shift;  // the first block's first position
+    const int64_t end = (int64_t)start + n;
+    const int group = warp >> (g.bs_shift - 4) << (g.bs_shift - 4);    // the first warp of this one's block
+    for (int64_t p0 = first; p0 < end; p0 += kPlaces) {
+        const int64_t mine = p0 + warp * kRows;                        // the warp's places, of one block
+        // lane i (and i + 16) looks up place i: its codes' row in the pool (-1: it gets none), their exponent
+        const int64_t p = mine + (lane & 15);
+        int64_t from = -1;
+        int e_from = INT_MIN;
+        const int64_t page = mine < end ? page_of_pos(mine) : -1;
         const int e_own = page >= 0 ? fp8_exp_of(g.scales[page]) : 0;
-        int e = off > 0 && page >= 0 ? e_own : INT_MIN;
-        bool bad = page < 0;
-        for (int i = lane; i < m; i += 32) {
-            int slot;
-            const int64_t from = source(r0 + i, slot);
-            if (from >= 0) e = max(e, fp8_exp_of(g.scales[from]));
-            else bad = true;
-        }
-        e = __reduce_max_sync(0xFFFFFFFFu, e);
-        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) flag(a.status, TQ_FLAG_BAD_SLOT);
-        if (page >= 0 && e != INT_MIN) {
-            uint8_t* dst = g.pool + page * stride;
-            for (int i0 = 0; i0 < m; i0 += kBatch) {  // a lane holds 4 codes of a row
-                uint32_t code[kBatch];
-                int d[kBatch];  // what the row's exponent changes by; 1: skipped
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    d[i] = 1;
-                    code[i] = 0;
-                    if (i0 + i < m) {
-                        int slot;
-                        const int64_t from = source(r0 + i0 + i, slot);
-                        if (from >= 0) {
-                            d[i] = (from == page ? e_own : fp8_exp_of(g.scales[from])) - e;
-                            code[i] = *(reinterpret_cast<const uint32_t*>(g.pool + from * stride + (int64_t)slot * kHeadDim) + lane);
-                        }
-                    }
+        if (page >= 0 && p < end) {
+            if (p < start) {
+                from = (page << g.bs_shift) + (p & (g.bs - 1));
+                e_from = e_own;
+            } else {
+                const int r = (int)(p - start), k = __ldg(a.kept + c0 + r);
+                const int64_t s = (int64_t)start + k, of = k >= r ? page_of_pos(s) : -1;
+                if (of >= 0) {
+                    from = (of << g.bs_shift) + (s & (g.bs - 1));
+                    e_from = fp8_exp_of(g.scales[of]);
                 }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (d[i] <= 0)
-                        *(reinterpret_cast<uint32_t*>(dst + (int64_t)(off + i0 + i) * kHeadDim) + lane) = scale_codes(code[i], d[i]);
-                __syncwarp();
             }
-            if (off > 0 && e > e_own) move_codes(dst, off, e_own - e);
-            __syncwarp();
-            if (lane == 0) g.scales[page] = fp8_pow2(e);
-            __syncwarp();
         }
-        r0 += m;
+        if (p >= start && p < end && from < 0 && lane < 16) flag(a.status, TQ_FLAG_BAD_SLOT);
+        // four rows at a time, 16 bytes a lane
+        uint4 code[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = __shfl_sync(0xFFFFFFFFu, from, 4 * i + (lane >> 3));
+            code[i] = make_uint4(0, 0, 0, 0);
+            if (row >= 0) code[i] = *(reinterpret_cast<const uint4*>(g.pool + row * kHeadDim) + (lane & 7));
+        }
+        const int top = __reduce_max_sync(0xFFFFFFFFu, e_from);
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();  // all rows are read, and all exponents
+        int e = INT_MIN;
+        for (int w = 0; w < g.bs >> 4; ++w) e = max(e, tops[group + w]);
+        if (page >= 0 && e != INT_MIN) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 4 * i + (lane >> 3);
+                const int64_t row = __shfl_sync(0xFFFFFFFFu, from, at);
+                const int d = __shfl_sync(0xFFFFFFFFu, e_from, at) - e;
+                const int64_t to = (page << g.bs_shift) + (mine & (g.bs - 1)) + at;
+                if (row >= 0 && (row != to || d != 0))
+                    *(reinterpret_cast<uint4*>(g.pool + to * kHeadDim) + (lane & 7)) =
+                        make_uint4(scale_codes(code[i].x, d), scale_codes(code[i].y, d), scale_codes(code[i].z, d), scale_codes(code[i].w, d));
+            }
+            if (warp == group && lane == 0 && e != e_own) g.scales[page] = fp8_pow2(e);
+        }
+        __syncthreads();  // (the next step reads what this one has not written, and tops again)
     }
 }
 
 }  // namespace
 
-bool fp8_keep_counts(const Fp8Geometry& g, int batch) { return (int64_t)batch * g.hkv * 2 / kWarps < (1 << 30); }
+bool fp8_keep_counts(const Fp8Geometry& g, int batch) { return (int64_t)batch * g.hkv * 2 < INT_MAX; }
 
 int launch_fp8_keep(const Fp8KeepArgs& a, void* stream) {
-    const int64_t warps = (int64_t)a.b.batch * a.g.hkv * 2;
-    return (int)launch_programmatic(fp8_keep_kernel, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0,
+    return (int)launch_programmatic(fp8_keep_kernel, dim3((unsigned)((int64_t)a.b.batch * a.g.hkv * 2)), dim3(kWarps * 32), 0,
                                     reinterpret_cast<cudaStream_t>(stream), a);
 }
 

@@ -21,16 +21,11 @@ struct Place {
     int head, side;
 };
 
-// Work item `w` (16 tokens) of the launch; 2^wpb_shift warps per block of tokens.
-__device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch& b, int64_t w, int wpb_shift,
-                                            int32_t* status) {
+// The 16 tokens from `first` on of unit u's block: everything but the head and the side.
+__device__ __forceinline__ Place place_of_unit(const Fp8Geometry& g, const Fp8Batch& b, uint32_t u, int first, int32_t* status) {
     Place p;
-    const int64_t item = w >> wpb_shift;
-    p.first = (int)(w & ((1 << wpb_shift) - 1)) * kRows;
-    p.side = (int)(item & 1);
-    const uint32_t uh = (uint32_t)(item >> 1);  // the host keeps the grid, and so this, below 2^31
-    const uint32_t u = uh / (uint32_t)g.hkv;
-    p.head = (int)(uh - u * (uint32_t)g.hkv);
+    p.first = first;
+    p.head = p.side = 0;
     p.live = false;
     p.blk = -1;
     p.row0 = 0;
@@ -54,6 +49,17 @@ __device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch
     p.pos = pos0 + p.first;
     p.lo = start > pos0 ? (int)(start - pos0) : 0;
     p.hi = (int)min((int64_t)g.bs, (int64_t)start + n - pos0);
+    return p;
+}
+// Work item `w` (16 tokens) of the launch; 2^wpb_shift warps per block of tokens.
+__device__ __forceinline__ Place find_place(const Fp8Geometry& g, const Fp8Batch& b, int64_t w, int wpb_shift,
+                                            int32_t* status) {
+    const int64_t item = w >> wpb_shift;
+    const uint32_t uh = (uint32_t)(item >> 1);  // the host keeps the grid, and so this, below 2^31
+    const uint32_t u = uh / (uint32_t)g.hkv;
+    Place p = place_of_unit(g, b, u, (int)(w & ((1 << wpb_shift) - 1)) * kRows, status);
+    p.side = (int)(item & 1);
+    p.head = (int)(uh - u * (uint32_t)g.hkv);
     return p;
 }
 // Whether the place's block lies in the pool (else it is flagged); its page is (blk * hkv + head) * 2 + side.

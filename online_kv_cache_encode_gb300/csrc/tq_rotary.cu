@@ -16,8 +16,8 @@ namespace {
 constexpr int kRotWarps = 8;
 constexpr int kRotHeads = 16;  // heads of a warp
 
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kRotWarps * 32) rotary_kernel(const RotaryArgs a) {
+template <typename T, bool INTER, bool WIDE>
+__global__ void __launch_bounds__(kRotWarps * 32, 3) rotary_kernel(const RotaryArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) rotary_kernel(const RotaryArgs
         if (lane == 0) flag(a.status, TQ_FLAG_BAD_SLOT);
         return;
     }
-    rotate_heads<T, WIDE>(a.r, a.r.table + (int64_t)p * a.r.rot, a.transpose != 0,
+    rotate_heads<T, INTER, WIDE, 4>(a.r, a.r.table + (int64_t)p * a.r.rot, a.transpose != 0,
                           static_cast<const T*>(a.x) + token * a.x_token + h0 * a.x_head, a.x_head,
                           static_cast<T*>(a.out) + token * a.out_token + h0 * a.out_head, a.out_head, min(kRotHeads, a.heads - h0), a.d);
 }
@@ -52,12 +52,16 @@ __global__ void rotary_table_kernel(const __grid_constant__ Frequencies f, int h
     }
 }
 
-template <typename T>
+template <typename T, bool INTER>
 int launch(const RotaryArgs& a, cudaStream_t s) {
     const int64_t warps = a.tokens * ((a.heads + kRotHeads - 1) / kRotHeads);
     const dim3 grid((unsigned)((warps + kRotWarps - 1) / kRotWarps)), block(kRotWarps * 32);
-    if (32 % (a.d / (2 * Elem<T>::V)) == 0) return (int)launch_programmatic(rotary_kernel<T, true>, grid, block, 0, s, a);
-    return (int)launch_programmatic(rotary_kernel<T, false>, grid, block, 0, s, a);
+    if (32 % (a.d / (2 * Elem<T>::V)) == 0) return (int)launch_programmatic(rotary_kernel<T, INTER, true>, grid, block, 0, s, a);
+    return (int)launch_programmatic(rotary_kernel<T, INTER, false>, grid, block, 0, s, a);
+}
+template <typename T>
+int launch(const RotaryArgs& a, cudaStream_t s) {
+    return a.r.interleaved ? launch<T, true>(a, s) : launch<T, false>(a, s);
 }
 
 }  // namespace
