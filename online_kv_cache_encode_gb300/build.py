@@ -23,7 +23,8 @@ SOURCES = [("tq_host.cpp", [], "tq_host.o"), ("tq_encode.cu", [], "tq_encode.o")
            ("tq_octopus.cu", [], "tq_octopus.o"), ("tq_selftest.cu", [], "tq_selftest.o"),
            ("tq_prefill_tc.cu", [], "tq_prefill_tc.o"), ("tq_fp8_host.cpp", [], "tq_fp8_host.o"),
            ("tq_fp8.cu", [], "tq_fp8.o"), ("tq_fp8_decode.cu", [], "tq_fp8_decode.o"),
-           ("tq_fp8_prefill.cu", [], "tq_fp8_prefill.o"), ("tq_fp8_append.cu", [], "tq_fp8_append.o"),
+           ("tq_fp8_prefill.cu", [], "tq_fp8_prefill.o"), ("tq_fp8_tree.cu", [], "tq_fp8_tree.o"),
+           ("tq_fp8_append.cu", [], "tq_fp8_append.o"),
            ("tq_fp8_keep.cu", [], "tq_fp8_keep.o"), ("tq_rotary_host.cpp", [], "tq_rotary_host.o"),
            ("tq_rotary.cu", [], "tq_rotary.o")]
 SOURCES += [("tq_inst.cu", [f"-DTQ_KB={kb}"], f"tq_inst_k{kb}.o") for kb in range(1, 9)]

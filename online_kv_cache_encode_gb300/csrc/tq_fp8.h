@@ -104,6 +104,9 @@ int launch_fp8_decode(const Fp8AttnArgs& a, const CUtensorMap& map, void* worksp
 bool fp8_prefill_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);  // the grid fits 32 bits
 size_t fp8_prefill_workspace(const Fp8Geometry& g, int64_t num_tokens, int batch, int group);
 int launch_fp8_prefill(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
+bool fp8_tree_counts(const Fp8Geometry& g, int64_t num_tokens, int batch, int group, int max_blocks);  // steps are counted in 32 bits
+size_t fp8_tree_workspace(const Fp8Geometry& g);
+int launch_fp8_tree(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspace, void* stream);
 
 }  // namespace tq
 

@@ -345,7 +345,9 @@ TQ_API tq_status tq_fp8_prefill_attention(const tq_fp8_cache* c, const void* q, 
 }
 
 TQ_API size_t tq_fp8_tree_workspace_bytes(const tq_fp8_cache* c, int64_t num_tokens, int batch, int num_q_heads) {
-    return tq_fp8_prefill_workspace_bytes(c, num_tokens, batch, num_q_heads);
+    if (!c || num_tokens <= 0 || num_tokens > INT_MAX || batch <= 0 || num_q_heads <= 0 || num_q_heads % c->g.hkv || num_q_heads / c->g.hkv > kFp8MaxGroup)
+        return 0;
+    return fp8_tree_workspace(c->g);
 }
 
 TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* c, const void* q, tq_dtype dtype, int64_t q_token_stride,
@@ -360,8 +362,8 @@ TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* c, const void* q, tq_
     if (st != TQ_OK) return st;
     if (!mask || misaligned(mask, 8)) return fail(TQ_ERR_INVALID_ARG, "mask must be non-NULL and 8-byte aligned");
     if (mask_words <= 0) return fail(TQ_ERR_INVALID_ARG, "mask_words must be positive");
-    if (!fp8_prefill_counts(c->g, num_tokens, batch, num_q_heads / c->g.hkv))
-        return fail(TQ_ERR_UNSUPPORTED, "more query rows than a launch holds");
+    if (!fp8_tree_counts(c->g, num_tokens, batch, num_q_heads / c->g.hkv, max_blocks_per_seq))
+        return fail(TQ_ERR_UNSUPPORTED, "tokens, heads and block table make 2^31 steps or more");
     if ((st = check_device(c)) != TQ_OK) return st;
     Fp8AttnArgs a{};
     a.g = c->g;
@@ -377,7 +379,7 @@ TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* c, const void* q, tq_
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     a.out = out;
     a.status = dev_status;
-    const int e = launch_fp8_prefill(a, c->side, workspace, stream);
+    const int e = launch_fp8_tree(a, c->side, workspace, stream);
     return e ? cuda_fail((cudaError_t)e, "tree attention launch") : TQ_OK;
 }
 

@@ -99,26 +99,6 @@ __device__ __forceinline__ Unit find_unit(const Fp8Batch& b, int u, int step) {
     return x;
 }
 
-__device__ __forceinline__ void pre_sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Eight columns of tensor memory.
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Notes the codes of NaN among the 32 tokens of a step that converter `cw` has: in `first` the first token of each dim that
 // holds one, in `any` of all dims, counted from the split's first token (t0 is the step's).  Rare, and out of line: inlined
 // it made the loop that calls it slower (a chunk of 4096 at 12288: 1368 us against 1345).
@@ -135,20 +115,7 @@ __device__ __noinline__ void note_nan(const uint8_t* codes, const int* exps, int
     }
 }
 
-// 32 bits of a row's mask: of nodes first .. first + 31 of its sequence's n (those before node 0 are the prefix, which every
-// row sees).
-__device__ __forceinline__ uint32_t seen_nodes(const uint64_t* mask, int words, int64_t first, int n) {
-    if (first + 32 <= 0) return 0xFFFFFFFFu;
-    const int at = (int)max(first, (int64_t)0), w = at >> 6, sh = at & 63;
-    uint64_t x = w < words ? __ldg(mask + w) >> sh : 0;
-    if (sh > 32 && w + 1 < words) x |= __ldg(mask + w + 1) << (64 - sh);
-    const int left = n - at;
-    uint32_t bits = left <= 0 ? 0u : left >= 32 ? (uint32_t)x : (uint32_t)x & ((1u << left) - 1);
-    if (first < 0) bits = (bits << (int)-first) | ((1u << (int)-first) - 1);
-    return bits;
-}
-
-template <typename T, int NT, int NP, bool TREE>  // NP: bf16 operands of the weights
+template <typename T, int NT, int NP>  // NP: bf16 operands of the weights
 __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs A, const __grid_constant__ CUtensorMap map) {
     using L = PreLayout<NT>;
     extern __shared__ uint8_t raw[];
@@ -214,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
     auto steps_of = [&](int x) {
         const int t0 = U.first + x * A.tpt;
         if (!U.live || t0 >= U.n) return 0;
-        const int64_t end = U.start < 0 ? 0 : min((int64_t)U.start + (TREE ? U.n : min(U.n, t0 + A.tpt)), cap);
+        const int64_t end = U.start < 0 ? 0 : min((int64_t)U.start + min(U.n, t0 + A.tpt), cap);
         return max(1, (int)((end + kTok - 1) / kTok));
     };
     const int nA = steps_of(0), nB = steps_of(1), nt = max(nA, nB);
@@ -230,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
     // id of the block that holds tokens 16 j .. of step u, or -1 (past the end) or -2 (not in the pool)
     auto block_of = [&](int u, int j) {
         const int64_t p = (int64_t)(s0 + u) * kTok + 16 * j;
-        const int64_t end = min((int64_t)U.start + (TREE ? U.n : min(U.n, U.first + 2 * A.tpt)), cap);
+        const int64_t end = min((int64_t)U.start + min(U.n, U.first + 2 * A.tpt), cap);
         if (U.start < 0 || p >= end) return -1;
         const int id = __ldg(A.a.b.block_table + (int64_t)U.b * A.a.b.max_blocks + (p >> g.bs_shift));
         return id >= 0 && id < g.num_blocks ? id : -2;
@@ -342,9 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 return y < 1e-37f ? 1e-37f : y;
             };
             const int limit = pos - u * kTok;  // the row sees tokens 0 .. limit of the tile
-            // a mask begins here, or a block is missing
-            const int64_t node0 = (int64_t)(s0 + u) * kTok - U.start;  // trees: the node that the step's first token is
-            const bool masked = ok != 0xFF || (TREE ? node0 + kTok > 0 : u * kTok + kTok - 1 > pos0);
+            const bool masked = ok != 0xFF || u * kTok + kTok - 1 > pos0;  // a mask begins here, or a block is missing
             wait(bS + x, u & 1);
             tc::fence_after_sync();
             __syncwarp();
@@ -357,22 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc::reg_fence(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
                 if (masked) {
-                    if constexpr (TREE) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint32_t bits = 0;
-                            if (there && U.start >= 0)
-                                bits = seen_nodes(A.a.mask + (U.row0 + tok) * A.a.words, A.a.words, node0 + 32 * w, U.n);
-                            bits &= ((ok >> (2 * w)) & 1 ? 0xFFFFu : 0u) | ((ok >> (2 * w + 1)) & 1 ? 0xFFFF0000u : 0u);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((bits >> j) & 1)) s[32 * w + j] = 0xFF800000u;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (j > limit || !((ok >> (j >> 4)) & 1)) s[j] = 0xFF800000u;
-                    }
+                    for (int j = 0; j < 128; ++j)
+                        if (j > limit || !((ok >> (j >> 4)) & 1)) s[j] = 0xFF800000u;
                 }
             };
             auto raise = [&](const uint32_t (&s)[128]) {
@@ -507,28 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 o[i + 2] = y;
             }
         };
-        // whether the row sees a token with a NaN in dim d: trees look for it among the nodes, where the first such token is one
-        auto sees_nan = [&](int d) -> bool {
-            if constexpr (!TREE) return nan_s[d] <= pos;
-            if (row < 0 || nan_s[d] == INT_MAX || U.start < 0) return false;
-            const int64_t first = (int64_t)s0 * kTok + nan_s[d] - U.start;
-            if (first < 0) return true;
-            const int64_t last = min((int64_t)U.n, min(cap, (int64_t)s1 * kTok) - U.start);
-            for (int64_t i = first; i < last; ++i) {
-                if (!(seen_nodes(A.a.mask + (int64_t)row * A.a.words, A.a.words, i, U.n) & 1)) continue;
-                const int64_t p = U.start + i;
-                const int id = __ldg(A.a.b.block_table + (int64_t)U.b * A.a.b.max_blocks + (p >> g.bs_shift));
-                if (id < 0 || id >= g.num_blocks) continue;
-                const int64_t at = ((((int64_t)id * g.hkv + h) * 2 + 1) << g.bs_shift) + (p & (g.bs - 1));
-                if ((__ldg(g.pool + at * kHeadDim + d) & 127) == 127) return true;
-            }
-            return false;
-        };
         // a dim is NaN from the first token on that has a NaN there: in the staged rows, dims d0 .. of `size` bytes
         auto spoil = [&](int d0, int n, int size) {
 #pragma unroll 1
-            for (int d = *any_nan <= (TREE ? INT_MAX - 1 : pos) ? 0 : n; d < n; ++d)
-                if (sees_nan(d0 + d)) {
+            for (int d = *any_nan <= pos ? 0 : n; d < n; ++d)
+                if (nan_s[d0 + d] <= pos) {
                     const uint32_t at = piece(d * size >> 4) + (d * size & 15);
                     if (size == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0x7FFF) : "memory");
                     else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0x7FFFFFFF) : "memory");
@@ -664,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
                 if (now == -2) flag(A.a.status, TQ_FLAG_BAD_SLOT);
                 if (u > 1 && __any_sync(0xFFFFFFFFu, bad)) break;
             }
-            if (lane == 0 && (U.start < 0 || (int64_t)U.start + (TREE ? U.n : min(U.n, U.first + 2 * A.tpt)) > cap)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+            if (lane == 0 && (U.start < 0 || (int64_t)U.start + min(U.n, U.first + 2 * A.tpt) > cap)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
             // copies may be in flight where a wait gave up: they end (again with a limit) before the memory is given back
             for (int u = max(0, sent - L::KS); u < sent; ++u) mbar_wait(bar(bK + u % L::KS), (u / L::KS) & 1);
             for (int u = max(0, sent - 2); u < sent; ++u) mbar_wait(bar(bV + (u & 1)), (u >> 1) & 1);
@@ -824,9 +759,9 @@ int splits_of(const Fp8Geometry& g, int64_t num_tokens, int batch, int group) {
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-template <typename T, int NT, int NP, bool TREE>
+template <typename T, int NT, int NP>
 int launch(const PreArgs& p, const CUtensorMap& map, int64_t units, cudaStream_t s) {
-    auto kern = fp8_prefill_kernel<T, NT, NP, TREE>;
+    auto kern = fp8_prefill_kernel<T, NT, NP>;
     static int done[64] = {};
     cudaError_t e = ensure_smem_limit(kern, PreLayout<NT>::smem, done);
     if (e != cudaSuccess) return (int)e;
@@ -865,9 +800,7 @@ int launch_fp8_prefill(const Fp8AttnArgs& a, const CUtensorMap& map, void* works
     p.ml = reinterpret_cast<float2*>(p.partials + (size_t)units * a.g.hkv * p.splits * kUnitRows * kHeadDim);
     p.stall_cycles = test_stall_cycles();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a.mask)
-        return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2, 1, true>(p, map, units, s) : launch<__half, 3, 2, true>(p, map, units, s);
-    return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2, 1, false>(p, map, units, s) : launch<__half, 3, 2, false>(p, map, units, s);
+    return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2, 1>(p, map, units, s) : launch<__half, 3, 2>(p, map, units, s);
 }
 
 }  // namespace tq
