@@ -180,8 +180,8 @@ __device__ __noinline__ void note_nan(const uint8_t* codes, const int* exps, int
 }
 
 // A bounded wait in few instructions (the waits are many, and what the warps execute together has to fit the SM's
-// instruction cache): `tries` tries that sleep for up to a microsecond each.
-constexpr int kTries = 1 << 20;
+// instruction cache): `tries` tries that sleep for about 4 us each where nothing arrives (7885 cycles measured), so a second.
+constexpr int kTries = 1 << 18;
 __device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, int tries) {
     uint32_t ok;
     asm volatile(
@@ -308,12 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
         return n ? Shape(n, end, A.tpt).size() * g.hkv : 0;
     };
     int* scan = reinterpret_cast<int*>(sm + L::mult);  // [16 warps]; the run's first sequence, the places before it, a sum
+    // (The host's limit keeps the places below 2^31 - 1, but cu_tokens that fall and rise again count tokens more than once.)
+    auto add = [](int x, int y) { return (int)min((uint32_t)x + (uint32_t)y, (uint32_t)INT_MAX); };
     // inclusive sum over the CTA, and the total
     auto sum_up = [&](int x, int& total) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-            if (lane >= o) x += y;
+            if (lane >= o) x = add(x, y);
         }
         __syncthreads();
         if (lane == 31) scan[warp] = x;
@@ -322,10 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
         total = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            before += w < warp ? scan[w] : 0;
-            total += scan[w];
+            before = add(before, w < warp ? scan[w] : 0);
+            total = add(total, scan[w]);
         }
-        return x + before;
+        return add(x, before);
     };
     int total = 0, mine = 0, upto = 0, first_part = 0;  // (the first 512 sequences' are kept)
     for (int b0 = 0; b0 < B; b0 += kThreads) {
@@ -337,7 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             upto = inc;
             first_part = part;
         }
-        total += part;
+        total = add(total, part);
+    }
+    if (total == INT_MAX) {
+        if (blockIdx.x == 0 && tid == 0) flag(A.a.status, TQ_FLAG_BAD_SLOT);
+        total = 0;
     }
     const int runs = min((int)gridDim.x, max(1, total / kLeastRun)), cta = (int)blockIdx.x;
     const int each = total / runs, more = total - each * runs;  // the first `more` runs have a place more
@@ -502,14 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                 __syncwarp();
                 // Masks and new references are rare, and go through tensor memory in loops of their own: what the turn's
                 // main path does not execute costs it instruction fetches all the same.
+                bool some = true;  // the row sees some of this thread's tokens
                 if (live && (ok != 0xFF || node0 + kTok > 0)) {
                     uint32_t bits = 0;
+                    some = false;
 #pragma unroll 1
                     for (int c = 4 * half; c < 4 * half + 4; ++c) {  // 16 tokens of a block
                         if (c & 1) bits >>= 16;
                         else bits = node >= 0 && it->start >= 0
                                         ? seen_nodes(A.a.mask + (int64_t)(it->row0 + node) * A.a.words, A.a.words, node0 + 16 * c, it->n) : 0u;
                         const uint32_t see = (ok >> c) & 1 ? bits : 0u;
+                        some |= (see & 0xFFFFu) != 0;
                         uint32_t y[16];
                         __syncwarp();
                         tmem_ld<16>(tS + 16 * c, y);
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                     f2_unpack(f2_add(part, part2), a, b);
                     a += b;
                     // one answer for all, and all have read their scores: their weights go where the other thread's lie
-                    const bool more_room = soft_barrier_or(!again && node >= 0 && (a > 64.f || (m == -INFINITY && a > 0.f)));
+                    const bool more_room = soft_barrier_or(!again && node >= 0 && (a > 64.f || (m == -INFINITY && some)));
                     if (more_room) {
                         raise();
                         continue;
@@ -936,6 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                     ++sp.unit;
                     if (sp.unit > sh.full || (sp.unit == sh.full && !sh.left)) {
                         sp.unit = 0;
+                        bool found = false;
                         for (++b;; b += 32) {
                             const int c = min(b + lane, B - 1);
                             int r0, st, en;
@@ -943,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                             const unsigned has = __ballot_sync(0xFFFFFFFFu, b + lane < B && nn > 0);
                             if (has || b + 32 >= B) {
                                 const int l = has ? __ffs((int)has) - 1 : 0;
+                                found = has;
                                 b = min(b + l, B - 1);
                                 n = __shfl_sync(0xFFFFFFFFu, nn, l);
                                 row0 = __shfl_sync(0xFFFFFFFFu, r0, l);
@@ -951,6 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                                 break;
                             }
                         }
+                        if (!found) break;  // (the inputs have changed since they were added up: the others' waits give up)
                         sh = Shape(n, end, A.tpt);
                     }
                     sp.one = sp.unit == sh.full;

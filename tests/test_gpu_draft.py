@@ -330,6 +330,52 @@ def test_tree_of_many_units(tq, dtype, hq, hkv, batch):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bs,hq,hkv,start,new", [(16, 5, 1, 20000, 60), (128, 7, 1, 9001, 200), (32, 3, 1, 30000, 1), (16, 33, 3, 4100, 13),
+                                                 (64, 128, 2, 2047, 5)])
+def test_tree_of_units_in_many_runs(tq, dtype, bs, hq, hkv, start, new):  # noqa: F811
+    """Few heads and nodes behind long prefixes: a unit is cut in up to as many runs as there are SMs, groups that do not
+    divide a tile, units of one row tile and of two; the same bytes again."""
+    gen = torch.Generator().manual_seed(start)
+    s = Setup(tq, gen, [start + new], hkv, bs)
+    s.fill([start + new])
+    see = DR.ancestors(DR.tree(new, gen))
+    q = torch.randn(new, hq, D, generator=gen).to(DT[dtype]).cuda()
+    out, flags = run_tree(tq, s, q, [start], [new], [see], -(-new // 64))
+    assert flags == 0
+    k, v = R.stored(s.pool, s.scales, s.rows[0], start + new)
+    check_tree(out, q, k, v, seen(start, see))
+    assert torch.equal(run_tree(tq, s, q, [start], [new], [see], -(-new // 64))[0], out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hkv,batch,empty", [(10, 2, 700, 0), (7, 1, 513, 512), (4, 2, 2600, 2100), (16, 16, 1100, 1099), (2, 1, 2000, 0)])
+def test_tree_of_many_sequences(tq, dtype, hq, hkv, batch, empty):  # noqa: F811
+    """Hundreds and thousands of sequences: the first `empty` and most of the others without nodes, trees that fill a tile
+    among those of one node; a sequence's rows are those that it has alone."""
+    gen = torch.Generator().manual_seed(batch)
+    news = torch.randint(1, 9, (batch,), generator=gen)
+    news[torch.rand(batch, generator=gen) < (0.8 if empty else 0.1)] = 0
+    news[:empty] = 0
+    news = news.tolist()
+    news[-1] = 70
+    starts = torch.randint(0, 200, (batch,), generator=gen).tolist()
+    lens = [a + n if n else 0 for a, n in zip(starts, news)]
+    s = Setup(tq, gen, [max(n, 1) for n in lens], hkv, 16)
+    s.fill([max(n, 1) for n in lens])
+    sees = [DR.ancestors(DR.tree(n, gen)) if n else torch.zeros(0, 0, dtype=torch.bool) for n in news]
+    q = torch.randn(sum(news), hq, D, generator=gen).to(DT[dtype]).cuda()
+    out, flags = run_tree(tq, s, q, starts, news, sees, 2)
+    assert flags == 0
+    cu = cu_of(news)
+    some = [b for b in range(batch) if news[b]]
+    for b in some[:20] + some[len(some) // 2:len(some) // 2 + 20] + some[-20:]:
+        k, v = R.stored(s.pool, s.scales, s.rows[b], lens[b])
+        check_tree(out[cu[b]:cu[b + 1]], q[cu[b]:cu[b + 1]], k, v, seen(starts[b], sees[b]))
+    assert not torch.isnan(out).any() and (out != 0).any(-1).all()
+    assert torch.equal(run_tree(tq, s, q, starts, news, sees, 2)[0], out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (20, 20)])
 def test_tree_that_is_a_chain_is_prefill(tq, dtype, hq, hkv):  # noqa: F811
     """Nodes in one line are a causal chunk: both calls against the same float64 form."""
@@ -397,6 +443,28 @@ def test_tree_values_at_the_limit_that_a_row_does_not_see(tq, dtype):  # noqa: F
     out, _ = run_tree(tq, s, q, [start], [n], [see], 1)
     k, v = R.stored(s.pool, s.scales, s.rows[0], start + n)
     check_tree(out, q, k, v, seen(start, see))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tree_rows_that_see_only_low_scores_behind_the_first_tile(tq, dtype):  # noqa: F811
+    """Rows that see nothing in the first 128 positions and scores of -180 and less behind them: their weights are as
+    good as any."""
+    gen = torch.Generator().manual_seed(64)
+    n = 270
+    s = Setup(tq, gen, [n], 1, 16)
+    signs = torch.where(torch.rand(D, generator=gen) < 0.5, -1.0, 1.0)
+    K, V = -4 * signs.expand(n, 1, D).bfloat16(), torch.randn(n, 1, D, generator=gen).bfloat16()
+    p, sc = R.write(s.pool.cpu(), s.scales.cpu(), K, V, [0, n], [0], s.rows)
+    s.pool.copy_(p)
+    s.scales.copy_(sc)
+    see = torch.rand(n, n, generator=gen) < 0.3
+    see[1::2, :129 + n // 8] = False
+    see[5] = False
+    q = (4 * signs + torch.randn(n, 2, D, generator=gen) / 4).to(DT[dtype]).cuda()
+    out, flags = run_tree(tq, s, q, [0], [n], [see], -(-n // 64))
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    check_tree(out, q, k, v, seen(0, see))
+    assert flags == 0 and not out[5].any() and (out[torch.arange(n) != 5] != 0).any(-1).all()
 
 
 def test_tree_nonfinite_query_and_scales(tq):  # noqa: F811
@@ -594,6 +662,37 @@ def test_two_streams_at_once(tq):  # noqa: F811
                 got.append((i, s.cache.tree(q, *args[i], mask)))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want[i]) for i, x in got)
+
+
+def test_two_graphs_at_once(tq):  # noqa: F811
+    """Two captured calls of one cache replayed on two streams without waiting for one another, and eager ones beside
+    them; then two captured with one workspace given, in turn."""
+    gen = torch.Generator().manual_seed(14)
+    lens = [2500, 900]
+    s = Setup(tq, gen, lens, 2, 16)
+    s.fill(lens)
+    q = torch.randn(30, 8, D, generator=gen).half().cuda()
+    mask = DR.mask_words([DR.ancestors(DR.tree(30, gen))], 1).cuda()
+    args = [(i32([0, 30]), i32([n - 30]), s.table[b:b + 1].contiguous(), mask) for b, n in enumerate(lens)]
+    want = [s.cache.tree(q, *a) for a in args]
+    ws = torch.zeros(tq.lib().tq_fp8_tree_workspace_bytes(s.cache._h, 30, 1, 8), dtype=torch.uint8, device="cuda")
+    for given in ({}, {"workspace": ws}):
+        graphs, outs = [], []
+        for a in args:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                outs.append(s.cache.tree(q, *a, **given))
+            graphs.append(graph)
+        streams = [torch.cuda.current_stream()] * 2 if given else [torch.cuda.Stream() for _ in args]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for graph, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    graph.replay()
+            eager = [s.cache.tree(q, *a, **given) for a in args]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, w) and torch.equal(e, w) for x, e, w in zip(outs, eager, want))
 
 
 def test_pool_beyond_32_bits(tq):  # noqa: F811
