@@ -14,24 +14,32 @@
 // head in the group): one row tile of 128 where that is enough (16 nodes of 8 query
 // heads), else two that see the same tokens.  A turn is one row tile over one tile of 128
 // tokens, and the tensor cores work on the scores of the next turn or two while the
-// softmax of this one runs.  All eight softmax warps work on every turn, two threads a row
-// with 64 tokens each: with one thread a row, and two row tiles (or every other token tile) in
-// turn, the chain scores -> weights -> output -> scores of a tile was what bounded a turn
-// (2450 cycles).
+// softmax of this one runs.  Eight warps share it, each half of them (a thread a row) with
+// every other turn: with two row tiles a half has one of them, with one the halves take
+// every other token tile of the same rows and hand the output's reference on.  References are
+// whole numbers, so that what was weighed against another one follows by a power of two.
+// Against all eight warps on every turn (64 tokens a thread, a barrier a turn): 64 trees of
+// 16 nodes over up to 16K tokens 286 -> 264 us, 8 of 33 over windows of 4096 57 -> 55,
+// one of 64 behind 32K 85 -> 89 (two row tiles: a half waits longer for its next scores), one
+// of 7 over 1K 17.8 -> 18.1.
 //
-// What bounds it: 1024 tensor cycles a turn (1792 with fp16 queries), 512 of exponentials,
-// and where a unit has one row tile about 1400 of shared memory (the operands of the scores
-// 512 and of the values 256, copies 256, V's conversion 384), against 1430 that HBM needs for
-// the 32 KB on one of 152 SMs.  The flat list of all token tiles (sequence, unit, head, tile) is cut into
-// equal runs, one CTA each, whatever the lengths are; a unit counts kUnitCost more, for its
-// start and end.  A unit that lies in one run is written directly; otherwise each
-// run leaves a partial (maximum, sum, output), which a second launch joins in their order,
-// so results do not depend on timing.
+// What bounds it: the chains between the warps.  A turn of one row tile has 1024 tensor
+// cycles (1792 with fp16 queries), 512 of exponentials and about 1400 of shared memory
+// (the operands of the scores 512 and of the values 256, copies 256, V's conversion 384), a tile
+// of tokens 1430 of HBM for its 32 KB on one of 152 SMs, and it takes 2350: V's conversion by
+// four warps 1480 and its waits for codes and a free operand, or where two row tiles share the
+// conversion, the issue of products (940 and 570 a turn) and the waits between them.
 //
-// Warps: 0-7 softmax and output, 8-11 V's conversion, 12 TMA, 13 MMA, 14 the list of items
-// and the scales, 15 the next unit's queries.  Tensor memory, in parts of 128 columns: one row
-// tile: three of scores (their weights overwrite them), one of output; two: two of scores, two
-// of outputs.
+// The flat list of all token tiles (sequence, unit, head, tile) is cut into equal runs, one
+// CTA each, whatever the lengths are; a unit counts kUnitCost more, for its start and end.
+// A unit that lies in one run is written directly; otherwise each run leaves a partial
+// (maximum, sum, output), which a second launch joins in their order, so results do not
+// depend on timing.
+//
+// Warps: 0-7 softmax and output, 8-11 V's conversion, 12 TMA of the keys, 13 MMA, 14 the
+// list of items, the scales and TMA of the values, 15 the next unit's queries.  Tensor memory,
+// in parts of 128 columns: one row tile: three of scores (their weights overwrite them), one
+// of output; two: two of scores, two of outputs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,16 +55,15 @@ constexpr int kRowsPerTile = 128;
 constexpr int kUnitRows = 256;
 constexpr int kTok = 128;   // tokens of a tile
 constexpr int kThreads = 512;
-constexpr int kMetaRing = 4;
-constexpr int kItemRing = 6;   // see the records below
 constexpr int kNanRing = 3;
 constexpr int kUseRing = 8;
 constexpr int kSoftRegs = 144, kOtherRegs = 112;  // of the two softmax warpgroups and the two others, out of 128 each
 constexpr float kHeadroom = 24.f;
 
 // What a run has of a unit.  Warp 14 goes through the list and leaves a record of every item, which all warps read.  A record
-// is written again six items on: the scales of an item's first tile wait for the product of the tile four before it, the item
-// in front of that had one too, and that product waits for the softmax warps to be done with the item before.
+// is written again IR items on, when the softmax warps, the last to need it, are done with it: the copy of the values of a
+// tile waits for the conversion of the tile VS before it, that one for the output of the tile two before it, and that for the
+// softmax warps' weights, which they form when they are done with the item before; every item has a tile at least.
 struct Item {
     int b, n, row0, start;   // the sequence, its nodes, packed row of the first, its position (negative: they see nothing)
     int end;                 // the tokens that there are: start + n, at most what the block table holds
@@ -77,21 +84,24 @@ template <int NT>
 struct TreeLayout {
     static constexpr int KS = 2;                        // stages of keys
     static constexpr int VS = NT == 2 ? 3 : 2;          // of codes of values: the wait for a copy and its conversion take longer than two turns
+    static constexpr int IR = NT == 2 ? 8 : 6;          // records of the list: VS + 4 at least, see above
+    static constexpr int MR = NT == 2 ? 8 : 6;          // tiles of scales: the same waits free them, VS + 3 at least
     static constexpr bool ahead = NT == 2;              // there is room for the next unit's queries
     static constexpr int q = 0;                         // [2 tiles][NT][128 rows][128 B], 128-byte swizzle
     static constexpr int k = q + 2 * NT * 16384;        // [KS][128 tokens][128 B], 128-byte swizzle
     static constexpr int v = k + KS * 16384;            // [VS][128 tokens][128 B] codes, 128-byte swizzle
     static constexpr int vb = v + VS * 16384;           // [2] bf16 operand: 8 x 8 core matrices, MN-major
     static constexpr int meta = vb + 2 * 32768;         // [ring]: key scales [8], value exponents [8] of 16 tokens each
-    static constexpr int okm = meta + kMetaRing * 64;   // [ring]: groups of 16 tokens that are there
-    static constexpr int items = okm + kMetaRing * 4;   // [ring] of Item
-    static constexpr int bars = items + kItemRing * (int)sizeof(Item);
-    static constexpr int nbars = 2 + 2 * KS + 2 * VS + 4 + 12 + 2 * kMetaRing + 1 + kItemRing + 2 + (ahead ? kUseRing : 0);
+    static constexpr int okm = meta + MR * 64;          // [ring]: groups of 16 tokens that are there
+    static constexpr int items = okm + MR * 4;          // [ring] of Item
+    static constexpr int bars = items + IR * (int)sizeof(Item);
+    static constexpr int nbars = 2 + KS + 2 * VS + 2 + 12 + MR + 1 + IR + 2 + (ahead ? kUseRing : 0);
     static constexpr int misc = bars + nbars * 8;       // tensor memory's address; the first token with a NaN in any dim [ring]
     static constexpr int mult = (misc + 16 + 15) / 16 * 16;  // [2][128] rows' score multipliers
     static constexpr int swap = ahead ? mult + 1024 : mult;  // [2][128] what the two threads of a row exchange
     static constexpr int total = swap + 1024;
     static constexpr int smem = total + 1008;           // the base is rounded up to 1 KB, from 16 bytes at least
+    static_assert(KS == 2 && MR >= VS + 3 && IR >= VS + 4 && IR <= kUseRing, "rings");
     static_assert(k % 1024 == 0 && v % 1024 == 0 && vb % 1024 == 0 && meta % 16 == 0 && bars % 8 == 0 && mult % 16 == 0, "alignment");
     static_assert(smem <= kSmemLimit, "tree attention does not fit in shared memory");
 };
@@ -245,12 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
     const Fp8Geometry& g = A.a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return sb + L::bars + 8 * i; };
-    // queries stored by the softmax warps, by warp 15; keys landed, free; codes of values landed, free;
-    // operand of values stored, free; scores, weights and output of a turn [4]; scales stored, free; outputs read; an item's
-    // record; all products done; one that nothing arrives on; an item's queries are in use [8]
-    constexpr int bQ = 0, bQa = 1, bK = 2, bKe = bK + L::KS, bV = bKe + L::KS, bVe = bV + L::VS, bB = bVe + L::VS, bBe = bB + 2,
-                  bS = bBe + 2, bP = bS + 4, bO = bP + 4, bM = bO + 4, bMe = bM + kMetaRing, bOe = bMe + kMetaRing, bR = bOe + 1,
-                  bEnd = bR + kItemRing, bNever = bEnd + 1, bQu = bNever + 1;
+    // queries stored by the softmax warps, by warp 15; keys landed; codes of values landed, free; operand of values stored;
+    // scores, weights and output of a turn [4]; scales stored; outputs read; an item's record; all products done; one that
+    // nothing arrives on; an item's queries are in use [8].  (The scores of the tile two before free a place of keys, its
+    // output one of the operands: no turn four later can be done by then, so the rings of 4 tell them apart.)
+    constexpr int bQ = 0, bQa = 1, bK = 2, bV = bK + L::KS, bVe = bV + L::VS, bB = bVe + L::VS,
+                  bS = bB + 2, bP = bS + 4, bO = bP + 4, bM = bO + 4, bOe = bM + L::MR, bR = bOe + 1,
+                  bEnd = bR + L::IR, bNever = bEnd + 1, bQu = bNever + 1;
     static_assert(bQu + (L::ahead ? kUseRing : 0) == L::nbars, "barriers");
 
     if (tid == 0) {
@@ -259,11 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
         for (int i = 0; i < (L::ahead ? kUseRing : 0); ++i) mbar_init(bar(bQu + i), 10);  // softmax, MMA, and warp 15 has the record
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(bB + i), 4);
-            mbar_init(bar(bBe + i), 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(bS + i), 1);
-            mbar_init(bar(bP + i), 8);
+            mbar_init(bar(bP + i), 4);
             mbar_init(bar(bO + i), 1);
         }
         for (int i = 0; i < L::VS; ++i) {
@@ -272,13 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
         }
         for (int i = 0; i < L::KS; ++i) {
             mbar_init(bar(bK + i), 1);
-            mbar_init(bar(bKe + i), 1);
         }
-        for (int i = 0; i < kMetaRing; ++i) {
+        for (int i = 0; i < L::MR; ++i) {
             mbar_init(bar(bM + i), 1);
-            mbar_init(bar(bMe + i), 1);
         }
-        for (int i = 0; i < kItemRing; ++i) mbar_init(bar(bR + i), 1);
+        for (int i = 0; i < L::IR; ++i) mbar_init(bar(bR + i), 1);
         mbar_init(bar(bOe), 8);
         mbar_init(bar(bEnd), 1);
         mbar_init(bar(bNever), 1);
@@ -388,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
     const Item* ring = reinterpret_cast<const Item*>(sm + L::items);
     // The record of the CTA's i-th item, or null where a wait gave up.
     auto record = [&](int i) -> const Item* {
-        wait(bR + i % kItemRing, (i / kItemRing) & 1);
-        return __any_sync(0xFFFFFFFFu, bad) ? nullptr : ring + i % kItemRing;
+        wait(bR + i % L::IR, (i / L::IR) & 1);
+        return __any_sync(0xFFFFFFFFu, bad) ? nullptr : ring + i % L::IR;
     };
     // id of the block that holds tokens 16 j .. of a tile, or -1 (past the end) or -2 (not in the pool)
     auto block_of = [&](int b, int end, int tile, int j) {
@@ -404,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
     if (!work) {
         if (tid == 0) A.joins[cta] = make_int4(0, 0, 0, 0);
     } else if (warp < 8) {
-        // ================= queries, softmax and output: two threads a row, of 64 tokens (and dims) each =================
+        // ================= queries, softmax, a thread a row in every other turn, and output, two threads a row =================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         float* const mult_s = reinterpret_cast<float*>(sm + L::mult);
         float* const swap_s = reinterpret_cast<float*>(sm + L::swap);
-        // What the other thread of the row has for x.
+        // what the thread of the row in the other half has for x
         auto exchange = [&](float x) {
             swap_s[half * 128 + r] = x;
             soft_barrier();
@@ -427,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             // These eight warps meet at barriers, so all of them have to go through the same items, also after a wait that
             // gave up.  Warp 14 leaves no record behind a wait of its own that did, and has left each of its records long
             // before these warps come to it: with four times its limit either all of them find one or none does.
-            if (!wait_tries(bar(bR + i % kItemRing), (i / kItemRing) & 1, 4 * kTries)) {
+            if (!wait_tries(bar(bR + i % L::IR), (i / L::IR) & 1, 4 * kTries)) {
                 bad = true;
                 break;
             }
             __syncwarp();
-            const Item* it = ring + i % kItemRing;
+            const Item* it = ring + i % L::IR;
             const bool one = it->flags & kOne;
             const int place = place_of(it, i);
             if (it->flags & kAhead) {
@@ -476,168 +484,164 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             }
             __syncwarp();
             if (L::ahead && lane == 0) mbar_arrive(bar(bQu + i % kUseRing));
-            // of the row in either tile: its factor, reference and sum; the tile whose turn it is comes first
-            float mult = mult_s[place * 128 + r], mult1 = one ? 0.f : mult_s[(place + 1) * 128 + r];
-            int node = it->first + r / G, node1 = node + A.tpt;  // -1: there is none
+            // Each half of these warps takes every other turn, a thread a row: with two row tiles its own, with one of the same
+            // rows, whose output they share.
+            const int mine = one ? 0 : half;
+            const float mult = mult_s[(place + mine) * 128 + r];
+            int node = it->first + mine * A.tpt + r / G;  // -1: there is none
             if (r >= A.tpt * G || node >= it->n) node = -1;
-            if (r >= A.tpt * G || node1 >= it->n) node1 = -1;
-            float m = -INFINITY, m1 = -INFINITY, sum = 0.f, sum1 = 0.f;
-            soft_barrier();  // the factors are read: their place may be written again
             // Warps without a node among their rows only meet the others: what lies in their rows reaches no other row.
-            bool live = __any_sync(0xFFFFFFFFu, node >= 0), live1 = __any_sync(0xFFFFFFFFu, node1 >= 0);
-            // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when
-            // the 64 weights of one of its threads add up to more than 64 (some weight is above 1 then; where it is not raised
-            // each is at most 64): bf16 and fp32 keep their precision at any size, the sum is needed anyway, and no maximum is formed
-            // otherwise.  The scores are still in tensor memory then, and the turn is weighed again.  A row that has seen no
-            // token yet has no reference.
+            const bool live = __any_sync(0xFFFFFFFFu, node >= 0);
+            // Weights are 2^(l - m) against a reference m, a whole number, that is put 2^24 above the row's maximum and raised again
+            // only when 32 weights add up to more than 32 (some weight is above 1 then): bf16 and fp32 keep their precision at
+            // any size, the sum is needed anyway, and no maximum is formed otherwise.  What was weighed before follows by a power of
+            // two, exactly.  A row that has seen no token yet has no reference.
+            float m = -INFINITY, sum = 0.f;
+            soft_barrier();  // the factors are read: their place may be written again
             const int tiles = it->tiles, turns = one ? tiles : 2 * tiles;
-            for (int u = 0; u < turns; ++u, ++turn) {
-                const int x = one ? 0 : u & 1, tu = one ? u : u >> 1, mi = (tile + tu) % kMetaRing;
-                const uint32_t tS = my + (one ? u % 3 : u & 1) * 128, tO = my + (one ? 384 : 256 + 128 * x);
-                wait(bM + mi, ((tile + tu) / kMetaRing) & 1);
+            // multiplies 8 columns of pairs of weights by a power of two
+            auto scale_weights = [&](uint32_t at, float by) {
+                uint32_t p = pack_bf16(by, by), y[8];
+                __syncwarp();
+                tmem_ld<8>(at, y);
+                tmem_ready<8>(y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], p);
+                tmem_st8(at, y);
+            };
+            for (int u = half; u < turns; u += 2) {
+                const int now = turn + u, tu = one ? u : u >> 1, mi = (tile + tu) % L::MR;
+                const uint32_t tS = my + (one ? u % 3 : u & 1) * 128, tO = my + (one ? 384 : 256 + 128 * half);
+                wait(bM + mi, ((tile + tu) / L::MR) & 1);
                 const int ok = *reinterpret_cast<const int*>(sm + L::okm + mi * 4);
-                const float* ks = reinterpret_cast<const float*>(sm + L::meta + mi * 64) + 4 * half;
-                auto factor = [&](int j) {  // of the thread's tokens 16 j .. (a masked score of -inf stays one; NaN stays NaN)
-                    const float y = ks[j] * mult;
-                    return y < 1e-37f ? 1e-37f : y;
-                };
+                const float* ks = reinterpret_cast<const float*>(sm + L::meta + mi * 64);
                 // the node that the tile's first token is: the masks begin behind the prefix
                 const int node0 = (it->tile0 + tu) * kTok - it->start;
-                wait(bS + (turn & 3), (turn >> 2) & 1);
+                wait(bS + (now & 3), (now >> 2) & 1);
                 tc::fence_after_sync();
                 __syncwarp();
-                // Masks and new references are rare, and go through tensor memory in loops of their own: what the turn's
-                // main path does not execute costs it instruction fetches all the same.
-                bool some = true;  // the row sees some of this thread's tokens
-                if (live && (ok != 0xFF || node0 + kTok > 0)) {
-                    uint32_t bits = 0;
-                    some = false;
+                if (live) {
+                    // Everything goes through tensor memory in loops that are not unrolled, the weights into the place of their
+                    // scores: with a turn's tokens in straight line, warps waited for instructions more than for anything else.
+                    if (ok != 0xFF || node0 + kTok > 0) {
+                        uint32_t bits = 0;
 #pragma unroll 1
-                    for (int c = 4 * half; c < 4 * half + 4; ++c) {  // 16 tokens of a block
-                        if (c & 1) bits >>= 16;
-                        else bits = node >= 0 && it->start >= 0
-                                        ? seen_nodes(A.a.mask + (int64_t)(it->row0 + node) * A.a.words, A.a.words, node0 + 16 * c, it->n) : 0u;
-                        const uint32_t see = (ok >> c) & 1 ? bits : 0u;
-                        some |= (see & 0xFFFFu) != 0;
-                        uint32_t y[16];
-                        __syncwarp();
-                        tmem_ld<16>(tS + 16 * c, y);
-                        tmem_ready<16>(y);
+                        for (int c = 0; c < 8; ++c) {  // 16 tokens, of a block
+                            if (c & 1) bits >>= 16;
+                            else bits = node >= 0 && it->start >= 0
+                                            ? seen_nodes(A.a.mask + (int64_t)(it->row0 + node) * A.a.words, A.a.words, node0 + 16 * c, it->n) : 0u;
+                            const uint32_t see = (ok >> c) & 1 ? bits : 0u;
+                            uint32_t y[16];
+                            __syncwarp();
+                            tmem_ld<16>(tS + 16 * c, y);
+                            tmem_ready<16>(y);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (!((see >> k) & 1)) y[k] = 0xFF800000u;
-                        tmem_st8(tS + 16 * c, *reinterpret_cast<uint32_t(*)[8]>(y));
-                        tmem_st8(tS + 16 * c + 8, *reinterpret_cast<uint32_t(*)[8]>(y + 8));
-                    }
-                    tc::wait_st();
-                }
-                // A new reference, the same in both threads of the row; all 256 threads come here together.
-                auto raise = [&] {
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = live ? 0 : 4; c < 4; ++c) {  // the scales are positive: maximum first, scale after
-                        uint32_t y[16];
-                        __syncwarp();
-                        tmem_ld<16>(tS + 64 * half + 16 * c, y);
-                        tmem_ready<16>(y);
-                        float z = -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) z = fmaxf(z, __uint_as_float(y[k]));
-                        mx = fmaxf(mx, z == -INFINITY ? z : z * factor(c));
-                    }
-                    mx = fmaxf(mx, exchange(mx));
-                    const bool rise = mx > m;
-                    const float fac = rise ? ex2(m - (mx + kHeadroom)) : 1.f;
-                    if (rise) m = mx + kHeadroom;
-                    sum *= fac;
-                    if (u > x && __any_sync(0xFFFFFFFFu, rise)) {  // the output, this thread's half
-                        const int last = turn - (one ? 1 : 2);
-                        wait(bO + (last & 3), (last >> 2) & 1);  // the row tile's turn before is complete
-                        tc::fence_after_sync();
-                        __syncwarp();
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[8];
-                            tmem_ld<8>(tO + 64 * half + 8 * c, o);
-                            tmem_ready<8>(o);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-                            tmem_st8(tO + 64 * half + 8 * c, o);
+                            for (int k = 0; k < 16; ++k)
+                                if (!((see >> k) & 1)) y[k] = 0xFF800000u;
+                            tmem_st8(tS + 16 * c, *reinterpret_cast<uint32_t(*)[8]>(y));
+                            tmem_st8(tS + 16 * c + 8, *reinterpret_cast<uint32_t(*)[8]>(y + 8));
                         }
                         tc::wait_st();
                     }
-                };
-                if (u <= x) raise();
-                for (bool again = false;; again = true) {
-                    if (!live) {
-                        if (!soft_barrier_or(false)) break;
-                        raise();
-                        continue;
-                    }
-                    uint32_t s[64], lo[NP == 2 ? 32 : 1];
-                    __syncwarp();
+#pragma unroll 1
+                    for (int c = 0, tried = 0; c < 4;) {  // 32 tokens; once more with a new reference
+                        uint32_t y[32], lo[16];
+                        __syncwarp();
+                        tc::ld_32x32b_x32(tS + 32 * c, y);
+                        // (a masked score of -inf stays one with a positive factor; NaN stays NaN)
+                        float f[2] = {ks[2 * c] * mult, ks[2 * c + 1] * mult};
+                        f[0] = f[0] < 1e-37f ? 1e-37f : f[0];
+                        f[1] = f[1] < 1e-37f ? 1e-37f : f[1];
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const uint64_t neg = f2_pack(-ref, -ref), f0 = f2_pack(f[0], f[0]), f1 = f2_pack(f[1], f[1]);
+                        uint64_t part = f2_pack(0.f, 0.f), part2 = part;
+                        tc::wait_ld();
+                        tc::reg_fence(y);
+                        uint32_t w[16];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tc::ld_32x32b_x32(tS + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-                    tc::wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tc::reg_fence(*reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-                    // the scores' weights, packed into the first half of s (their remainders into lo), and their sum
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const uint64_t neg = f2_pack(-ref, -ref);
-                    uint64_t part = f2_pack(0.f, 0.f), part2 = part, f2;
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        if (j % 16 == 0) {
-                            const float y = factor(j >> 4);
-                            f2 = f2_pack(y, y);
+                        for (int k = 0; k < 16; ++k) {
+                            float a, b;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), k < 8 ? f0 : f1, neg), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            if (k & 1) part = f2_add(part, f2_pack(a, b));
+                            else part2 = f2_add(part2, f2_pack(a, b));
+                            w[k] = pack_bf16(a, b);
+                            if constexpr (NP == 2) lo[k] = pack_bf16(a - __uint_as_float(w[k] << 16), b - __uint_as_float(w[k] & 0xFFFF0000u));
                         }
                         float a, b;
-                        // a masked score is -inf: its product with a positive scale too
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, neg), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        if (j & 2) part = f2_add(part, f2_pack(a, b));
-                        else part2 = f2_add(part2, f2_pack(a, b));
-                        s[j / 2] = pack_bf16(a, b);
-                        if constexpr (NP == 2)
-                            lo[j / 2] = pack_bf16(a - __uint_as_float(s[j / 2] << 16), b - __uint_as_float(s[j / 2] & 0xFFFF0000u));
+                        f2_unpack(f2_add(part, part2), a, b);
+                        a += b;
+                        if (!tried && __any_sync(0xFFFFFFFFu, node >= 0 && (a > 32.f || m == -INFINITY))) {
+                            tried = 1;
+                            // a new reference; the scores are still there
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                uint32_t z = y[k];
+                                if (__uint_as_float(z) != -INFINITY) mx = fmaxf(mx, __uint_as_float(z) * f[k >> 4]);
+                            }
+                            float by = 1.f;
+                            if (mx > m) {
+                                const float to = ceilf(mx) + kHeadroom;
+                                by = ex2(m - to);
+                                m = to;
+                            }
+                            sum *= by;
+#pragma unroll 1
+                            for (int k = 0; k < c; ++k)
+                                for (int z = 0; z < 2 * NP; ++z) scale_weights(tS + 32 * k + 8 * z, by);
+                            tc::wait_st();
+                            continue;
+                        }
+                        sum += a;
+                        tc::st_32x32b_x16(tS + 32 * c, w);
+                        if constexpr (NP == 2) tc::st_32x32b_x16(tS + 32 * c + 16, lo);
+                        ++c;
+                        tried = 0;
                     }
-                    float a, b;
-                    f2_unpack(f2_add(part, part2), a, b);
-                    a += b;
-                    // one answer for all, and all have read their scores: their weights go where the other thread's lie
-                    const bool more_room = soft_barrier_or(!again && node >= 0 && (a > 64.f || (m == -INFINITY && some)));
-                    if (more_room) {
-                        raise();
-                        continue;
-                    }
-                    sum += a;
-                    tc::st_32x32b_x32(tS + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(s));
-                    if constexpr (NP == 2) tc::st_32x32b_x32(tS + 64 + 32 * half, lo);
                     tc::wait_st();
-                    break;
                 }
+                // The output's reference is the one of the turn before it: with one row tile the other half's.
+                const bool follows = one ? u > 0 : u > 1;
+                if (one && follows) wait(bP + ((now - 1) & 3), ((now - 1) >> 2) & 1);
+                __syncwarp();
+                if (live && follows) {
+                    const float before = swap_s[mine * 128 + r];
+                    if (__any_sync(0xFFFFFFFFu, before != m)) {
+                        const float to = fmaxf(before, m);
+                        const float by_w = to == m ? 1.f : ex2(m - to), by_o = to == before ? 1.f : ex2(before - to);
+                        m = to;
+                        sum *= by_w;
+                        if (__any_sync(0xFFFFFFFFu, by_w != 1.f)) {
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k)
+                                for (int z = 0; z < 2 * NP; ++z) scale_weights(tS + 32 * k + 8 * z, by_w);
+                        }
+                        if (__any_sync(0xFFFFFFFFu, by_o != 1.f)) {
+                            const int last = now - (one ? 1 : 2);
+                            wait(bO + (last & 3), (last >> 2) & 1);
+                            tc::fence_after_sync();
+                            __syncwarp();
+#pragma unroll 1
+                            for (int c = 0; c < 16; ++c) {
+                                uint32_t o[8];
+                                tmem_ld<8>(tO + 8 * c, o);
+                                tmem_ready<8>(o);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by_o);
+                                tmem_st8(tO + 8 * c, o);
+                            }
+                        }
+                        tc::wait_st();
+                    }
+                }
+                swap_s[mine * 128 + r] = m;
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bP + (turn & 3)));
-                if (!one) {  // the other tile's turn
-                    float y = m;
-                    m = m1;
-                    m1 = y;
-                    y = sum;
-                    sum = sum1;
-                    sum1 = y;
-                    y = mult;
-                    mult = mult1;
-                    mult1 = y;
-                    const int z = node;
-                    node = node1;
-                    node1 = z;
-                    const bool w = live;
-                    live = live1;
-                    live1 = w;
-                }
+                if (lane == 0) mbar_arrive(bar(bP + (now & 3)));
             }
+            turn += turns;
             // ---- the item's end ----
             tile += tiles;
             for (int k = 1; k <= (one ? 1 : 2); ++k) {
@@ -645,6 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                 __syncwarp();
             }
             tc::fence_after_sync();
+            // With one row tile both halves have sums of the same rows, and the output has the last turn's reference.
+            soft_barrier();
+            const float last_m = one ? swap_s[r] : m;
+            soft_barrier();
+            if (one) sum = sum == 0.f ? 0.f : sum * ex2(m - last_m);
+            m = last_m;
             if (bad && !empty) {
                 flag(A.a.status, TQ_FLAG_TIMEOUT);
                 empty = true;
@@ -655,26 +665,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             const bool nan_here = any_nan[nan_slot] != INT_MAX;
 #pragma unroll 1
             for (int x = 0; x < (one ? 1 : 2); ++x) {
-                if (x) {
-                    m = m1;
-                    sum = sum1;
-                    node = node1;
-                    live = live1;
-                }
                 const uint32_t tO = my + (one ? 384 : 256 + 128 * x) + 64 * half;
-                sum += exchange(sum);
-                const bool none = sum == 0.f;
-                const float inv = whole && !none ? 1.f / sum : 1.f;
+                // sums and references: of either half's turns, or of the half that has the tile
+                const float other = exchange(sum);
+                soft_barrier();
+                const float other_m = exchange(m);
+                const float all = one ? sum + other : half == x ? sum : other, ref = one || half == x ? m : other_m;
+                const int node_x = it->first + x * A.tpt + r / G, row_node = r < A.tpt * G && node_x < it->n ? node_x : -1;
+                const bool live_x = __any_sync(0xFFFFFFFFu, row_node >= 0);
+                const bool none = all == 0.f;
+                const float inv = whole && !none ? 1.f / all : 1.f;
                 if (!whole && half == 0)
-                    A.ml[slot * kUnitRows + x * 128 + r] = make_float2(none || empty ? -INFINITY : m, none || empty ? 0.f : sum);
+                    A.ml[slot * kUnitRows + x * 128 + r] = make_float2(none || empty ? -INFINITY : ref, none || empty ? 0.f : all);
                 // A dim is NaN in the rows that see a token with a NaN there: all, where the first such position is in the prefix.
                 auto sees_nan = [&](int d) -> bool {
                     const int at = __ldcg(nan_g + nan_slot * kHeadDim + d);
-                    if (node < 0 || at == INT_MAX) return false;
+                    if (row_node < 0 || at == INT_MAX) return false;
                     if (at < it->start) return true;
                     const int last = min(it->end, (it->tile0 + tiles) * kTok);
                     for (int p = at; p < last; ++p) {
-                        if (!(seen_nodes(A.a.mask + (int64_t)(it->row0 + node) * A.a.words, A.a.words, p - it->start, it->n) & 1)) continue;
+                        if (!(seen_nodes(A.a.mask + (int64_t)(it->row0 + row_node) * A.a.words, A.a.words, p - it->start, it->n) & 1)) continue;
                         const int id = __ldg(A.a.b.block_table + (int64_t)it->b * A.a.b.max_blocks + (p >> g.bs_shift));
                         if (id < 0 || id >= g.num_blocks) continue;
                         const int64_t row = ((((int64_t)id * g.hkv + it->head) * 2 + 1) << g.bs_shift) + (p & (g.bs - 1));
@@ -689,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                 auto piece = [&](int k) { return at + r * 256 + ((k ^ (lane & 7)) << 4); };
 #pragma unroll 1
                 for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
-                    if (live && (whole || pass == half)) {
+                    if (live_x && (whole || pass == half)) {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t o[16];
@@ -762,16 +772,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
         // ================= V: codes to bf16, times the block's scale =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         const int cw = warp - 8;
-        int t = 0;
+        int t = 0, turn = 0, last1 = 0, last2 = 0;  // last turns of the two tiles before
         for (int i = 0;; ++i) {
             const Item* it = record(i);
             if (!it) break;
+            const int per_tile = it->flags & kOne ? 1 : 2;
             const int p_item = it->tile0 * kTok, end = it->end, last = it->flags & kLast, t_item = t, t_end = t + it->tiles;
             for (; t < t_end; ++t) {
-                const int b = t & 1, vi = t % L::VS, mi = t % kMetaRing;
-                wait(bM + mi, (t / kMetaRing) & 1);
-                wait(bV + vi, (t / L::VS) & 1);
-                if (t > 1) wait(bBe + b, ((t - 2) >> 1) & 1);
+                const int b = t & 1, vi = t % L::VS, mi = t % L::MR;
+                wait(bV + vi, (t / L::VS) & 1);  // (warp 14 has written the scales before it arrives there)
+                if (t > 1) wait(bO + (last2 & 3), (last2 >> 2) & 1);
+                last2 = last1;
+                last1 = (turn += per_tile) - 1;
                 const int* vs = reinterpret_cast<const int*>(sm + L::meta + mi * 64 + 32);
                 // A warp converts 32 tokens, of two groups of 16 with a scale each: 8 of them by 4 pieces of 16 codes at a
                 // time.  What a lane reads and writes differs by constants from one time to the next.  (Unrolled by 8 it is slower, as all
@@ -841,17 +853,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             asm volatile("fence.proxy.async.global;" ::: "memory");  // the codes were written by ordinary stores
             const int per = g.bs >> 4;  // groups of 16 tokens in a block
             int t = 0, sent = 0;  // tiles whose copies are issued: none behind one whose wait gave up
+            int turn = 0, last1 = 0, last2 = 0;  // last turns of the two tiles before
             for (int i = 0; !__any_sync(0xFFFFFFFFu, bad); ++i) {
                 const Item* it = record(i);
                 if (!it) break;
-                const int b = it->b, end = it->end, h = it->head, tile0 = it->tile0, tiles = it->tiles, last = it->flags & kLast;
+                const int b = it->b, end = it->end, h = it->head, tile0 = it->tile0, tiles = it->tiles, last = it->flags & kLast, per_tile = it->flags & kOne ? 1 : 2;
                 if (lane == 0 && (it->start < 0 || end < (int64_t)it->start + it->n)) flag(A.a.status, TQ_FLAG_BAD_SLOT);
                 int id = lane < pages ? block_of(b, end, tile0, lane * per) : -1;
                 for (int u = 0; u < tiles; ++u, ++t) {
                     const int now = id, ks = t % L::KS;
                     id = lane < pages && u + 1 < tiles ? block_of(b, end, tile0 + u + 1, lane * per) : -1;
                     const unsigned there = __ballot_sync(0xFFFFFFFFu, now >= 0);
-                    if (t >= L::KS) wait(bKe + ks, (t / L::KS - 1) & 1);
+                    if (t >= L::KS) wait(bS + (last2 & 3), (last2 >> 2) & 1);
+                    last2 = last1;
+                    last1 = (turn += per_tile) - 1;
                     if (__any_sync(0xFFFFFFFFu, bad)) break;
                     sent = t + 1;
                     if (lane == 0) mbar_arrive_tx(bar(bK + ks), (uint32_t)__popc(there) * bytes);
@@ -881,10 +896,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                 to_go -= at1 - sp.at;
                 if (tiles > 0) {
                     // (warp 15 has read what is written over)
-                    if (L::ahead && i >= kItemRing) wait(bQu + (i - kItemRing) % kUseRing, ((i - kItemRing) / kUseRing) & 1);
+                    if (L::ahead && i >= L::IR) wait(bQu + (i - L::IR) % kUseRing, ((i - L::IR) / kUseRing) & 1);
                     if (__any_sync(0xFFFFFFFFu, bad)) break;
                     if (lane == 0) {
-                        Item* it = reinterpret_cast<Item*>(sm + L::items) + i % kItemRing;
+                        Item* it = reinterpret_cast<Item*>(sm + L::items) + i % L::IR;
                         it->b = b;
                         it->n = n;
                         it->row0 = row0;
@@ -897,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                         it->flags = (sp.one ? kOne : 0) | (to_go <= kUnitCost ? kLast : 0) | (tile0 == 0 && tiles == sh.tiles ? kWhole : 0) |
                                     (tile0 == 0 ? kBegins : 0) | (L::ahead && sp.one && was_one ? kAhead : 0);
                         it->runs = run_of(t1 - to_go - at1 + sp.size - (sp.one ? 1 : 2)) - cta + 1;  // (up to the one with its last tile)
-                        mbar_arrive(bar(bR + i % kItemRing));
+                        mbar_arrive(bar(bR + i % L::IR));
                     }
                     __syncwarp();
                     was_one = sp.one;
@@ -909,11 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                     int id = lane < 8 ? block_of(b, end, tile0, lane) : -1, id1 = lane < 8 && tiles > 1 ? block_of(b, end, tile0 + 1, lane) : -1;
                     float2 sc = scales_of(id);
                     for (int u = 0; u < tiles; ++u, ++t) {
-                        const int mi = t % kMetaRing, vs = t % L::VS;
+                        const int mi = t % L::MR, vs = t % L::VS;
                         const int id2 = lane < 8 && u + 2 < tiles ? block_of(b, end, tile0 + u + 2, lane) : -1;
                         const float2 sc1 = scales_of(id1);
                         const unsigned ok = __ballot_sync(0xFFFFFFFFu, id >= 0);
-                        if (t >= kMetaRing) wait(bMe + mi, (t / kMetaRing - 1) & 1);
                         if (__any_sync(0xFFFFFFFFu, bad)) break;
                         if (lane < 8) {
                             // where there is no block any positive scale does: the scores are masked
@@ -1003,7 +1017,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
 #pragma unroll
                             for (int k = 0; k < 4; ++k) mma_f8_ss(d, q + j * 1024 + 2 * k, kk + 2 * k, idesc_f8(128, false), j > 0 || k > 0);
                         tc::commit(bar(bS + ((turn + u) & 3)));
-                        if (one || x) tc::commit(bar(bKe + ks));
                     }
                     __syncwarp();
                 };
@@ -1023,12 +1036,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
 #pragma unroll
                         for (int j = 0; j < NP; ++j)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) tc::mma_f16_ts(d, s + 64 * j + 8 * k, v + 16 * k, idesc_v, u > x || j > 0 || k > 0);
+                            for (int k = 0; k < 8; ++k) tc::mma_f16_ts(d, s + 32 * (k >> 1) + 8 * (k & 1) + 16 * j, v + 16 * k, idesc_v, u > x || j > 0 || k > 0);
                         tc::commit(bar(bO + ((turn + u) & 3)));
-                        if (one || x) {  // for all rows
-                            tc::commit(bar(bBe + vb));
-                            tc::commit(bar(bMe + tu % kMetaRing));
-                        }
                     }
                     __syncwarp();
                     if (__any_sync(0xFFFFFFFFu, bad)) break;
