@@ -5,8 +5,8 @@
 // the nodes j with bit j in its row of a mask:
 //   out_i = sum_t w_t V_t / sum_t w_t,  w_t = exp(s_t - m),  t < start or bit (t - start) of mask_i
 //   S [128 rows x 128 tokens] = Q . K^T    kind::f8f6f4, the query in two or three e4m3 terms, K as its codes
-//   O [128 rows x 128 dims]  += P . V      kind::f16, bf16 weights (fp16 queries: and their remainders), V's codes
-//                                          times their scale converted to bf16
+//   O [128 rows x 128 dims]  += P . V      kind::f16, bf16 weights (fp16 queries and small calls: and their
+//                                          remainders), V's codes times their scale converted to bf16
 // The operands and their roundings are those of the causal kernel for chunks; what differs
 // is that all rows of a tree see the whole prefix, and that there are few of them.
 //
@@ -1151,6 +1151,13 @@ __global__ void __launch_bounds__(256) fp8_tree_join_kernel(const TreeArgs A) {
     *(reinterpret_cast<uint2*>(out) + lane) = make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));
 }
 
+// Up to that many places a run, the weights of bf16 queries go to the tensor cores with their remainders, too.  Weights
+// rounded to 8 bits put as much error into an output as its own rounding on average, but three times that into single rows (a
+// few tokens with large values that cancel); a batch of many rows hides that, a call of a few does not, and is short enough:
+// 7 nodes over 1K 18.1 -> 20.5 us, error 0.0041 -> 0.0019 of the output (its rounding alone: 0.0019).  64 nodes over 32K
+// (82 places a run) would go from 89 to 106 us, 64 x 16 over up to 16K from 265 to 301, errors from 0.0023 to 0.0016.
+constexpr int64_t kExactRun = 16;
+
 int tokens_per_tile(int group) { return kRowsPerTile / group; }
 
 // At least as many places as the list can have.
@@ -1204,7 +1211,8 @@ int launch_fp8_tree(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspac
     const int64_t most = most_places(a.g, a.b.num_tokens, a.b.batch, a.group, a.b.max_blocks);
     const int grid = (int)(most / kLeastRun < runs ? most / kLeastRun < 1 ? 1 : most / kLeastRun : runs);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2, 1>(p, map, grid, s) : launch<__half, 3, 2>(p, map, grid, s);
+    if (a.dtype != TQ_BF16) return launch<__half, 3, 2>(p, map, grid, s);
+    return most <= kExactRun * runs ? launch<__nv_bfloat16, 2, 2>(p, map, grid, s) : launch<__nv_bfloat16, 2, 1>(p, map, grid, s);
 }
 
 }  // namespace tq

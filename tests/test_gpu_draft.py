@@ -213,21 +213,23 @@ def test_append_without_a_place(tq):  # noqa: F811
 
 
 # --------------------------------------------------------------------------- tree
-def check_tree(out, q, k, v, see, sm_scale=1 / math.sqrt(D)):
+def check_tree(out, q, k, v, see, sm_scale=1 / math.sqrt(D), weights=None):
     """test_gpu_fp8.check() with any truth values: the same roundings of weights, scores and the output.  And what is
-    below every type's range: a weight is held in bf16 against a reference at most 2^24 above the row's largest, so one
-    below 2^-133 (bf16's smallest number) of the reference, 2^-109 of the largest weight, and so of their sum, may count
-    as 0; an output below the type's smallest number is off by up to that."""
+    below every type's range: a weight is formed in fp32 against a reference at most 2^25 above the row's largest (a
+    whole number of octaves, 24 above), and one below 2^-126 (fp32's smallest normal number) of the reference, 2^-101 of
+    the largest weight, and so of their sum, may count as 0; an output below the type's smallest number is off by up to
+    that."""
     nan = (see[:, None, :, None] & (torch.isnan(v) | torch.isnan(k).any(-1, keepdim=True))[None]).any(2)
     nan = nan.repeat_interleave(q.shape[1] // k.shape[0], 1)
     assert torch.equal(torch.isnan(out), nan)
     clean = lambda x: torch.where(torch.isnan(x), torch.zeros_like(x), x)  # noqa: E731
     want, spread, sharp = DR.attend(q, clean(k), clean(v), see, sm_scale, PREFILL)
     eps = torch.finfo(out.dtype).eps
-    weights = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -12
+    if weights is None:
+        weights = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -12
     tol = eps / 2 * want.abs() + spread * (weights + 2.0 ** -19 + 2 * 2.0 ** -16 * sharp[..., None])
     tol = tol + (2.0 ** -25 if out.dtype == torch.float16 else 2.0 ** -134)  # subnormals
-    tol = tol + see.shape[1] * 2.0 ** -109 * clean(v).abs().max()
+    tol = tol + see.shape[1] * 2.0 ** -101 * clean(v).abs().max()
     err = torch.where(nan, torch.zeros_like(want), (out.double() - want).abs())
     assert not torch.isinf(out).any()
     assert (err <= tol).all(), float((err / tol.clamp(min=1e-300)).max())
@@ -443,6 +445,22 @@ def test_tree_values_at_the_limit_that_a_row_does_not_see(tq, dtype):  # noqa: F
     out, _ = run_tree(tq, s, q, [start], [n], [see], 1)
     k, v = R.stored(s.pool, s.scales, s.rows[0], start + n)
     check_tree(out, q, k, v, seen(start, see))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hkv,start,new", [(1, 1, 1017, 7), (8, 2, 300, 20), (4, 4, 3000, 3)])
+def test_tree_of_a_small_call_keeps_its_weights(tq, dtype, hq, hkv, start, new):  # noqa: F811
+    """Few rows: weights and their remainders, both rounded to bf16, off by 2^-9 * 2^-9 at most (2^-17 with the sum's
+    fp32 roundings in proportion), also where values of other sizes cancel."""
+    gen = torch.Generator().manual_seed(65)
+    s = Setup(tq, gen, [start + new], hkv, 16)
+    s.fill([start + new])
+    see = DR.ancestors(DR.tree(new, gen))
+    q = (2 * torch.randn(new, hq, D, generator=gen)).to(DT[dtype]).cuda()
+    out, flags = run_tree(tq, s, q, [start], [new], [see], 1)
+    assert flags == 0
+    k, v = R.stored(s.pool, s.scales, s.rows[0], start + new)
+    check_tree(out, q, k, v, seen(start, see), weights=2.0 ** -17)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
