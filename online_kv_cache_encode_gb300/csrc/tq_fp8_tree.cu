@@ -1151,12 +1151,12 @@ __global__ void __launch_bounds__(256) fp8_tree_join_kernel(const TreeArgs A) {
     *(reinterpret_cast<uint2*>(out) + lane) = make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));
 }
 
-// Up to that many places a run, the weights of bf16 queries go to the tensor cores with their remainders, too.  Weights
-// rounded to 8 bits put as much error into an output as its own rounding on average, but three times that into single rows (a
-// few tokens with large values that cancel); a batch of many rows hides that, a call of a few does not, and is short enough:
-// 7 nodes over 1K 18.1 -> 20.5 us, error 0.0041 -> 0.0019 of the output (its rounding alone: 0.0019).  64 nodes over 32K
-// (82 places a run) would go from 89 to 106 us, 64 x 16 over up to 16K from 265 to 301, errors from 0.0023 to 0.0016.
-constexpr int64_t kExactRun = 16;
+// Up to that many query rows, the weights of bf16 queries go to the tensor cores with their remainders, too.  Weights rounded
+// to 8 bits put as much error into an output as its own rounding on average, but three times that into single rows (a few
+// tokens with large values that cancel); a call of many rows hides that and has the more products, one of a few does not:
+// 7 rows over 1K 18.1 -> 20.5 us, error 0.0041 -> 0.0019 of the output (its rounding alone: 0.0019); 4096 rows over 32K would go
+// from 89 to 106 us, 32768 over up to 16K from 265 to 301, errors from 0.0023 to 0.0016.
+constexpr int64_t kExactRows = 1024;
 
 int tokens_per_tile(int group) { return kRowsPerTile / group; }
 
@@ -1212,7 +1212,7 @@ int launch_fp8_tree(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspac
     const int grid = (int)(most / kLeastRun < runs ? most / kLeastRun < 1 ? 1 : most / kLeastRun : runs);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (a.dtype != TQ_BF16) return launch<__half, 3, 2>(p, map, grid, s);
-    return most <= kExactRun * runs ? launch<__nv_bfloat16, 2, 2>(p, map, grid, s) : launch<__nv_bfloat16, 2, 1>(p, map, grid, s);
+    return a.b.num_tokens * a.hq <= kExactRows ? launch<__nv_bfloat16, 2, 2>(p, map, grid, s) : launch<__nv_bfloat16, 2, 1>(p, map, grid, s);
 }
 
 }  // namespace tq

@@ -428,7 +428,8 @@ def test_tree_nan_codes(tq, dtype, bs, hq, hkv, start, new):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_tree_values_at_the_limit_that_a_row_does_not_see(tq, dtype):  # noqa: F811
+@pytest.mark.parametrize("hq", [4, 20])
+def test_tree_values_at_the_limit_that_a_row_does_not_see(tq, dtype, hq):  # noqa: F811
     """Nodes whose values are 2^128, past what bf16 holds, and keys that dominate: no trace in the rows without them."""
     gen = torch.Generator().manual_seed(63)
     start, n = 50, 60
@@ -441,7 +442,7 @@ def test_tree_values_at_the_limit_that_a_row_does_not_see(tq, dtype):  # noqa: F
     s.scales.copy_(sc)
     see = DR.ancestors(DR.tree(n, gen))
     see[:, 14:30] = False
-    q = torch.randn(n, 4, D, generator=gen).to(DT[dtype]).cuda()
+    q = torch.randn(n, hq, D, generator=gen).to(DT[dtype]).cuda()
     out, _ = run_tree(tq, s, q, [start], [n], [see], 1)
     k, v = R.stored(s.pool, s.scales, s.rows[0], start + n)
     check_tree(out, q, k, v, seen(start, see))
@@ -464,7 +465,8 @@ def test_tree_of_a_small_call_keeps_its_weights(tq, dtype, hq, hkv, start, new):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_tree_rows_that_see_only_low_scores_behind_the_first_tile(tq, dtype):  # noqa: F811
+@pytest.mark.parametrize("hq", [2, 5])
+def test_tree_rows_that_see_only_low_scores_behind_the_first_tile(tq, dtype, hq):  # noqa: F811
     """Rows that see nothing in the first 128 positions and scores of -180 and less behind them: their weights are as
     good as any."""
     gen = torch.Generator().manual_seed(64)
@@ -478,20 +480,21 @@ def test_tree_rows_that_see_only_low_scores_behind_the_first_tile(tq, dtype):  #
     see = torch.rand(n, n, generator=gen) < 0.3
     see[1::2, :129 + n // 8] = False
     see[5] = False
-    q = (4 * signs + torch.randn(n, 2, D, generator=gen) / 4).to(DT[dtype]).cuda()
+    q = (4 * signs + torch.randn(n, hq, D, generator=gen) / 4).to(DT[dtype]).cuda()
     out, flags = run_tree(tq, s, q, [0], [n], [see], -(-n // 64))
     k, v = R.stored(s.pool, s.scales, s.rows[0], n)
     check_tree(out, q, k, v, seen(0, see))
     assert flags == 0 and not out[5].any() and (out[torch.arange(n) != 5] != 0).any(-1).all()
 
 
-def test_tree_nonfinite_query_and_scales(tq):  # noqa: F811
+@pytest.mark.parametrize("hq", [8, 60])
+def test_tree_nonfinite_query_and_scales(tq, hq):  # noqa: F811
     """A NaN or an infinity in a query row makes its own row NaN; scores of both signs and sizes; sm_scale."""
     gen = torch.Generator().manual_seed(6)
     s = Setup(tq, gen, [300], 1, 16)
     s.fill([300])
     see = DR.ancestors(DR.tree(20, gen))
-    q = torch.randn(20, 8, D, generator=gen).bfloat16().cuda()
+    q = torch.randn(20, hq, D, generator=gen).bfloat16().cuda()
     q[3] *= 2.0 ** -60
     q[4] *= 30
     good, _ = run_tree(tq, s, q, [280], [20], [see], 1, sm_scale=0.3)
@@ -500,7 +503,7 @@ def test_tree_nonfinite_query_and_scales(tq):  # noqa: F811
     bad = q.clone()
     bad[2, 2, 7], bad[9, 5, 9] = math.nan, math.inf
     out, _ = run_tree(tq, s, bad, [280], [20], [see], 1, sm_scale=0.3)
-    rest = torch.ones(20, 8, dtype=torch.bool)
+    rest = torch.ones(20, hq, dtype=torch.bool)
     rest[2, 2] = rest[9, 5] = False
     assert torch.equal(out[rest.cuda()], good[rest.cuda()]) and torch.isnan(out[~rest.cuda()]).all()
 
