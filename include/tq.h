@@ -596,8 +596,11 @@ TQ_API tq_status tq_fp8_append(const tq_fp8_cache* cache, const void* K, const v
  * sequence whose bit is set in its row of the mask (device uint64
  * [num_tokens, mask_words], 8-byte aligned; bit j % 64 of word j / 64): itself
  * only if its own bit is set, none from 64 * mask_words on, and bits from n on
- * do not count.  A row that attends to nothing is zero.  Everything else is as
- * for tq_fp8_prefill_attention, the precision and the workspace's rules too. */
+ * do not count.  A row that attends to nothing is zero.  Each weight is rounded
+ * to 2^-16 of itself, for bf16 queries too, whatever else is in the call (rows
+ * that belong to no sequence change no byte of the others; another sequence may
+ * change the order of sums).  Everything else is as for
+ * tq_fp8_prefill_attention, the workspace's rules too. */
 TQ_API size_t tq_fp8_tree_workspace_bytes(const tq_fp8_cache* cache, int64_t num_tokens, int batch, int num_q_heads);
 TQ_API tq_status tq_fp8_tree_attention(const tq_fp8_cache* cache, const void* q, tq_dtype dtype, int64_t q_token_stride,
                                        int64_t q_head_stride, int64_t num_tokens, int batch, int num_q_heads,

@@ -5,10 +5,11 @@
 // the nodes j with bit j in its row of a mask:
 //   out_i = sum_t w_t V_t / sum_t w_t,  w_t = exp(s_t - m),  t < start or bit (t - start) of mask_i
 //   S [128 rows x 128 tokens] = Q . K^T    kind::f8f6f4, the query in two or three e4m3 terms, K as its codes
-//   O [128 rows x 128 dims]  += P . V      kind::f16, bf16 weights (fp16 queries and small calls: and their
-//                                          remainders), V's codes times their scale converted to bf16
-// The operands and their roundings are those of the causal kernel for chunks; what differs
-// is that all rows of a tree see the whole prefix, and that there are few of them.
+//   O [128 rows x 128 dims]  += P . V      kind::f16, weights as bf16 and their remainders as bf16, V's codes times
+//                                          their scale converted to bf16
+// The operands are those of the causal kernel for chunks; what differs is that all rows of a tree see the
+// whole prefix, that there are few of them, and that bf16 queries' weights keep their remainders too: a
+// weight rounded to 8 bits puts three times the output's own rounding into rows whose values cancel.
 //
 // A unit is up to 256 query rows of one sequence and KV head (row = token * group + query
 // head in the group): one row tile of 128 where that is enough (16 nodes of 8 query
@@ -246,7 +247,7 @@ __device__ __forceinline__ void store_terms(const uint4 (&raw)[K], uint8_t* plac
     if (col < K) mult[row + 2 * col] = factors;
 }
 
-template <typename T, int NT, int NP>  // NP: bf16 operands of the weights
+template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap map) {
     using L = TreeLayout<NT>;
     extern __shared__ uint8_t raw[];
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                             if (k & 1) part = f2_add(part, f2_pack(a, b));
                             else part2 = f2_add(part2, f2_pack(a, b));
                             w[k] = pack_bf16(a, b);
-                            if constexpr (NP == 2) lo[k] = pack_bf16(a - __uint_as_float(w[k] << 16), b - __uint_as_float(w[k] & 0xFFFF0000u));
+                            lo[k] = pack_bf16(a - __uint_as_float(w[k] << 16), b - __uint_as_float(w[k] & 0xFFFF0000u));
                         }
                         float a, b;
                         f2_unpack(f2_add(part, part2), a, b);
@@ -590,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                             sum *= by;
 #pragma unroll 1
                             for (int k = 0; k < c; ++k)
-                                for (int z = 0; z < 2 * NP; ++z) scale_weights(tS + 32 * k + 8 * z, by);
+                                for (int z = 0; z < 4; ++z) scale_weights(tS + 32 * k + 8 * z, by);
                             tc::wait_st();
                             continue;
                         }
                         sum += a;
                         tc::st_32x32b_x16(tS + 32 * c, w);
-                        if constexpr (NP == 2) tc::st_32x32b_x16(tS + 32 * c + 16, lo);
+                        tc::st_32x32b_x16(tS + 32 * c + 16, lo);
                         ++c;
                         tried = 0;
                     }
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                         if (__any_sync(0xFFFFFFFFu, by_w != 1.f)) {
 #pragma unroll 1
                             for (int k = 0; k < 4; ++k)
-                                for (int z = 0; z < 2 * NP; ++z) scale_weights(tS + 32 * k + 8 * z, by_w);
+                                for (int z = 0; z < 4; ++z) scale_weights(tS + 32 * k + 8 * z, by_w);
                         }
                         if (__any_sync(0xFFFFFFFFu, by_o != 1.f)) {
                             const int last = now - (one ? 1 : 2);
@@ -1034,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                         const uint32_t s = tmem + (one ? u % 3 : u & 1) * 128, d = tmem + (one ? 384 : 256 + 128 * x);
                         const uint64_t v = d_v + vb * 2048;
 #pragma unroll
-                        for (int j = 0; j < NP; ++j)
+                        for (int j = 0; j < 2; ++j)  // the weights, their remainders
 #pragma unroll
                             for (int k = 0; k < 8; ++k) tc::mma_f16_ts(d, s + 32 * (k >> 1) + 8 * (k & 1) + 16 * j, v + 16 * k, idesc_v, u > x || j > 0 || k > 0);
                         tc::commit(bar(bO + ((turn + u) & 3)));
@@ -1151,13 +1152,6 @@ __global__ void __launch_bounds__(256) fp8_tree_join_kernel(const TreeArgs A) {
     *(reinterpret_cast<uint2*>(out) + lane) = make_uint2(pack_two<T>(o4.x * inv, o4.y * inv), pack_two<T>(o4.z * inv, o4.w * inv));
 }
 
-// Up to that many query rows, the weights of bf16 queries go to the tensor cores with their remainders, too.  Weights rounded
-// to 8 bits put as much error into an output as its own rounding on average, but three times that into single rows (a few
-// tokens with large values that cancel); a call of many rows hides that and has the more products, one of a few does not:
-// 7 rows over 1K 18.1 -> 20.5 us, error 0.0041 -> 0.0019 of the output (its rounding alone: 0.0019); 4096 rows over 32K would go
-// from 89 to 106 us, 32768 over up to 16K from 265 to 301, errors from 0.0023 to 0.0016.
-constexpr int64_t kExactRows = 1024;
-
 int tokens_per_tile(int group) { return kRowsPerTile / group; }
 
 // At least as many places as the list can have.
@@ -1169,9 +1163,9 @@ int64_t most_places(const Fp8Geometry& g, int64_t num_tokens, int batch, int gro
 
 int runs_of(const Fp8Geometry& g) { return g.num_sms > 0 ? g.num_sms : 1; }
 
-template <typename T, int NT, int NP>
+template <typename T, int NT>
 int launch(const TreeArgs& p, const CUtensorMap& map, int grid, cudaStream_t s) {
-    auto kern = fp8_tree_kernel<T, NT, NP>;
+    auto kern = fp8_tree_kernel<T, NT>;
     static int done[64] = {};
     cudaError_t e = ensure_smem_limit(kern, TreeLayout<NT>::smem, done);
     if (e != cudaSuccess) return (int)e;
@@ -1211,8 +1205,7 @@ int launch_fp8_tree(const Fp8AttnArgs& a, const CUtensorMap& map, void* workspac
     const int64_t most = most_places(a.g, a.b.num_tokens, a.b.batch, a.group, a.b.max_blocks);
     const int grid = (int)(most / kLeastRun < runs ? most / kLeastRun < 1 ? 1 : most / kLeastRun : runs);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype != TQ_BF16) return launch<__half, 3, 2>(p, map, grid, s);
-    return a.b.num_tokens * a.hq <= kExactRows ? launch<__nv_bfloat16, 2, 2>(p, map, grid, s) : launch<__nv_bfloat16, 2, 1>(p, map, grid, s);
+    return a.dtype == TQ_BF16 ? launch<__nv_bfloat16, 2>(p, map, grid, s) : launch<__half, 3>(p, map, grid, s);
 }
 
 }  // namespace tq
