@@ -589,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                                 m = to;
                             }
                             sum *= by;
+                            tc::wait_st();  // the weights of the chunks before, which are read again
 #pragma unroll 1
                             for (int k = 0; k < c; ++k)
                                 for (int z = 0; z < 4; ++z) scale_weights(tS + 32 * k + 8 * z, by);

@@ -1,4 +1,6 @@
 """Attention of trees of drafts on the GPU: what weights, masks and queries may hold."""
+import math
+
 import pytest
 import torch
 
@@ -47,3 +49,40 @@ def test_tree_rows_of_no_sequence_change_no_byte(tq, dtype):  # noqa: F811
     out = torch.full((T + more, hq, D), 7.0, dtype=DT[dtype], device="cuda")
     s.cache.tree(q, i32(cu_of(news)), i32(starts), s.table, mask, out=out)
     assert torch.equal(out[:T], alone) and (out[T:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,new", [(1, 100), (4, 30), (2, 100), (8, 16)])   # of one row tile and of two
+@pytest.mark.parametrize("start", [0, 284])
+@pytest.mark.parametrize("steps", [(0, 26, 52, 80), (0, 0, 32, 0), (80, 0, 0, 80), (0, 32, 0, 64)])
+def test_tree_references_raised_within_a_tile(tq, dtype, hq, new, start, steps):  # noqa: F811
+    """Scores that rise by tens of octaves from one 32 tokens of a tile to the next, and rows that see their first token
+    in any of them, so that weights that are already formed are scaled again, in some rows of a warp and not in others;
+    values as large as the weights are small, so that every weight counts in the output."""
+    gen = torch.Generator().manual_seed(hq + sum(steps))
+    n = start + new
+    s = Setup(tq, gen, [n], 1, 16)
+    # dim 0 carries the step of a token's 32 (halves of the steps are exact in e4m3): with 16 in a query's dim 0 its
+    # score is that many octaves, and the product of weight and value about 1
+    step = torch.tensor(steps, dtype=torch.float32)[torch.arange(n) % 128 // 32]
+    K, V = torch.randn(n, 1, D, generator=gen) / 4, torch.randn(n, 1, D, generator=gen)
+    K[:, 0, 0] = step / 2
+    V *= torch.exp2(80 - step)[:, None, None]
+    p, sc = R.write(s.pool.cpu(), s.scales.cpu(), K, V, [0, n], [0], s.rows)
+    s.pool.copy_(p)
+    s.scales.copy_(sc)
+    most = float(step.max())
+    if dtype == "f16":   # (outputs within the type's range)
+        s.scales[:, :, 1] *= 2.0 ** (most - 80)
+    q = torch.randn(new, hq, D, generator=gen)
+    q[..., 0] = torch.tensor([16.0, 8.0, 20.0, 0.0] if dtype == "bf16" else [16.0, 20.0, 16.0, 24.0])[torch.arange(new) % 4][:, None]
+    q = q.to(DT[dtype]).cuda()
+    see = DR.ancestors(DR.tree(new, gen))
+    if start == 0 and dtype == "f16":   # (a row that sees no token of the largest step would be past it)
+        see[:, int(step.argmax())] = True
+    sm_scale = math.log(2) / 8
+    out, flags = run_tree(tq, s, q, [start], [new], [see], 2, sm_scale=sm_scale)
+    assert flags == 0
+    k, v = R.stored(s.pool, s.scales, s.rows[0], n)
+    check_tree(out, q, k, v, seen(start, see), sm_scale, weights=2.0 ** -17)
+    assert torch.equal(run_tree(tq, s, q, [start], [new], [see], 2, sm_scale=sm_scale)[0], out)
