@@ -488,7 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
             // Each half of these warps takes every other turn, a thread a row: with two row tiles its own, with one of the same
             // rows, whose output they share.
             const int mine = one ? 0 : half;
-            const float mult = mult_s[(place + mine) * 128 + r];
+            const float factor = mult_s[(place + mine) * 128 + r];
+            // A query that is not finite has a factor of NaN. Its row goes along with another one, so that masked scores stay
+            // -inf, and its sum becomes NaN at the item's end if it has seen anything.
+            const bool odd = factor != factor;
+            const float mult = odd ? 1.f : factor;
             int node = it->first + mine * A.tpt + r / G;  // -1: there is none
             if (r >= A.tpt * G || node >= it->n) node = -1;
             // Warps without a node among their rows only meet the others: what lies in their rows reaches no other row.
@@ -651,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tree_kernel(const TreeArgs A,
                 __syncwarp();
             }
             tc::fence_after_sync();
+            if (odd && sum != 0.f) sum = NAN;
             // With one row tile both halves have sums of the same rows, and the output has the last turn's reference.
             soft_barrier();
             const float last_m = one ? swap_s[r] : m;

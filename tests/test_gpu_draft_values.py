@@ -86,3 +86,38 @@ def test_tree_references_raised_within_a_tile(tq, dtype, hq, new, start, steps):
     k, v = R.stored(s.pool, s.scales, s.rows[0], n)
     check_tree(out, q, k, v, seen(start, see), sm_scale, weights=2.0 ** -17)
     assert torch.equal(run_tree(tq, s, q, [start], [new], [see], 2, sm_scale=sm_scale)[0], out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq", [1, 8, 60])
+def test_tree_nonfinite_queries_that_see_nothing(tq, dtype, hq):  # noqa: F811
+    """A row that attends to nothing is zero whatever its query holds (a padded step's rows may hold anything): by its
+    mask, by a negative start, by blocks that are not there; one that sees a token is NaN, also where the unit is cut and
+    where it sees nothing in most of the tiles; the others keep their bytes."""
+    gen = torch.Generator().manual_seed(hq)
+    starts, news = [0, -7, 20, 3000], [300, 9, 12, 40]
+    lens = [max(a, 0) + n for a, n in zip(starts, news)]
+    s = Setup(tq, gen, lens, 1, 16)
+    s.fill(lens)
+    table = s.table.clone()
+    table[2, :3] = -1
+    sees = [DR.ancestors(DR.tree(n, gen)) for n in news]
+    sees[0][::3] = False
+    sees[0][9, 290] = sees[0][12, 3] = True      # one token, in the last tile and in the first
+    q = torch.randn(sum(news), hq, D, generator=gen).to(DT[dtype]).cuda()
+    cu, mask = cu_of(news), DR.mask_words(sees, 5).cuda()
+    good = s.cache.tree(q, i32(cu), i32(starts), table, mask)
+    bad = q.clone()
+    spoilt = torch.zeros(sum(news), hq, dtype=torch.bool)
+    for row, x in ((0, math.nan), (3, math.inf), (6, -math.inf), (9, math.nan), (12, math.inf), (5, math.nan), (299, math.inf), (301, math.nan),
+                   (305, math.inf), (310, math.nan), (320, -math.inf), (330, math.nan), (331, math.inf)):
+        spoilt[row, row % hq] = True
+        bad[row, row % hq, row % D] = x
+    st = tq.new_status()
+    out = s.cache.tree(bad, i32(cu), i32(starts), table, mask, status=st)
+    assert st.item() == tq.FLAG_BAD_SLOT
+    nothing = torch.cat((~sees[0].any(1), torch.ones(9 + 12, dtype=torch.bool), torch.zeros(40, dtype=torch.bool)))
+    assert not out[nothing.cuda()].any() and not good[nothing.cuda()].any()
+    nan = spoilt & ~nothing[:, None]
+    assert torch.isnan(out[nan.cuda()]).all() and nan.sum() == 6
+    assert torch.equal(out[~nan.cuda()], good[~nan.cuda()])
