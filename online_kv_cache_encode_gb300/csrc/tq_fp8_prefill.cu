@@ -289,9 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
         }
         if (steps > 0) wait(bQ + x, 0);
         __syncwarp();
-        const float mult = steps > 0 ? mult_s[r] : 0.f;
-        // the row's place in the output waits there meanwhile: registers are what the loop lacks
-        reinterpret_cast<int*>(mult_s)[r] = there ? (int)(U.row0 + tok) : -1;
+        float mult = steps > 0 ? mult_s[r] : 0.f;
+        // the row's place in the output waits there meanwhile: registers are what the loop lacks (-1: there is none)
+        int place = there ? (int)(U.row0 + tok) : -1;
+        // A query that is not finite has a factor of NaN. Its row goes along with another one, so that masked scores stay
+        // -inf, and its sum becomes NaN at the end if it has seen anything; its place is noted below -1.
+        if (mult != mult) {
+            mult = 1.f;
+            if (there) place = -2 - place;
+        }
+        reinterpret_cast<int*>(mult_s)[r] = place;
         // Weights are 2^(l - m) against a reference m that is put 2^24 above the row's maximum and raised again only when
         // the 128 weights of a step add up to more than 128 (some weight is above 1 then; where it is not raised each is at
         // most 128): bf16 and fp32 keep their precision at any size, the sum is needed anyway, and no maximum is formed
@@ -431,7 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_prefill_kernel(const PreArgs 
             tc::fence_after_sync();
             __syncwarp();
         }
-        const int row = reinterpret_cast<const int*>(mult_s)[r];
+        int row = reinterpret_cast<const int*>(mult_s)[r];
+        if (row < -1) {
+            row = -2 - row;
+            if (sum != 0.f) sum = NAN;
+        }
         int cta;
         asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));  // (read again, not held)
         const int uh2 = cta / A.splits, h2 = uh2 % A.a.g.hkv;

@@ -152,3 +152,34 @@ def test_any_bytes_behind_the_end_of_a_block_of_the_largest_scale(tq, call):  # 
     else:
         out = s.cache.prefill(q, i32([0, 5]), i32([32]), s.table)
     check(out, q, k, v, [33, 34, 35, 36, 37], DECODE if call == "decode" else PREFILL)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,long", [(1, 300), (8, 4000), (40, 300)])
+def test_nonfinite_queries_that_see_nothing(tq, dtype, hq, long):  # noqa: F811
+    """Rows with a negative start or without a block that is there are zero whatever their queries hold, as a decode's
+    rows of no length are; rows that see a token are NaN, the others keep their bytes."""
+    gen = torch.Generator().manual_seed(hq)
+    starts, news = [-5, 20, long - 12, 0], [10, 12, 12, 40]
+    lens = [300, 300, long, 40]
+    s = Setup(tq, gen, lens, 1, 16)
+    s.fill(lens)
+    table = s.table.clone()
+    table[1] = -1
+    table[3, :2] = -1                                    # rows 0 .. 31 of the fourth see nothing, 32 .. some tokens
+    q = torch.randn(sum(news), hq, D, generator=gen).to(DT[dtype]).cuda()
+    nothing = torch.zeros(sum(news), dtype=torch.bool)
+    nothing[:22] = nothing[34:66] = True
+    nan = torch.zeros(sum(news), hq, dtype=torch.bool)
+    bad = q.clone()
+    for row, x in ((0, math.nan), (9, math.inf), (10, math.nan), (21, -math.inf), (22, math.nan), (33, math.inf), (34, math.nan), (65, math.inf),
+                   (66, math.inf), (70, math.nan)):
+        bad[row, row % hq, row % D] = x
+        nan[row, row % hq] = not nothing[row]
+    good = s.cache.prefill(q, i32(cu_of(news)), i32(starts), table)
+    out = s.cache.prefill(bad, i32(cu_of(news)), i32(starts), table)
+    assert not out[nothing.cuda()].any() and not good[nothing.cuda()].any()
+    assert torch.isnan(out[nan.cuda()]).all() and nan.sum() == 4
+    assert torch.equal(out[~nan.cuda()], good[~nan.cuda()])
+    out = s.cache.decode(bad[[0, 10, 22]], table[:3].contiguous(), i32([0, 100, long]))
+    assert not out[:2].any() and torch.isnan(out[2, 22 % hq]).all()
