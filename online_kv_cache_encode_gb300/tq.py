@@ -422,8 +422,10 @@ class Rotary:
                  table: torch.Tensor | None = None, device="cuda"):
         if layout not in _ROTARY_LAYOUTS:
             raise TQError(TQ_ERR_INVALID_ARG, f"bad rotary layout {layout!r}")
-        if dim <= 0 or dim % 16 or dim > 256 or num_positions <= 0:
+        if dim <= 0 or dim % 16 or dim > 256:
             raise TQError(TQ_ERR_UNSUPPORTED, "the rotated dims must be a multiple of 16, at most 256")
+        if num_positions <= 0:
+            raise TQError(TQ_ERR_UNSUPPORTED, "the table's positions must be positive")
         self.dim, self.num_positions, self.layout = dim, num_positions, layout
         self._layout, self._lib = _ROTARY_LAYOUTS[layout], lib()
         if table is None:

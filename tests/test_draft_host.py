@@ -131,3 +131,9 @@ def test_mask_words_and_trees():
     one = torch.zeros(1, 130, dtype=torch.bool)
     one[0, 63] = one[0, 64] = one[0, 129] = True
     assert DR.mask_words([one], 3).tolist() == [[-1 << 63, 1, 2]]
+
+
+@pytest.mark.parametrize("dim,far,what", [(24, 10, "dims"), (0, 10, "dims"), (272, 10, "dims"), (64, 0, "positions"), (64, -1, "positions")])
+def test_rotary_says_what_is_wrong(tq, dim, far, what):  # noqa: F811
+    with pytest.raises(tq.TQError, match=what):
+        tq.Rotary(dim, far)
