@@ -85,7 +85,9 @@ constexpr int kAppendCtaWarps = sizeof(T) == 4 ? kAppendWarps / 2 : kAppendWarps
 // What bounds it is instructions as much as bytes (a rotated and coded element is 8 of them).  32K x 8 heads of bf16: a
 // warp a side and an item, two CTAs an SM, 87 us; keys rotated a second time instead of held in registers, three CTAs an
 // SM, 62; a warp for both sides 56, all of these without the next item's rows on their way; with them 40 (4.6 TB/s, issue
-// active 36 % with 16 warps an SM; the codes of 33 MB stay in L2).
+// active 36 % with 16 warps an SM; the codes of 33 MB stay in L2).  fp32 rows, 8 warps of 156 registers: 70, 0.76 of the
+// copy's rate.  With the queries of 64 heads 230, of 32 136: CTAs of queries have an SM to themselves, one at a time, as the
+// launch gives them the others' shared memory; a call without queries and one of the rotation take 220 and 133.
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kAppendCtaWarps<T> * 32, 1) fp8_append_kernel(const Fp8AppendArgs a, int wpb_shift, uint32_t items, uint32_t kv_grid) {
     using E = Elem<T>;

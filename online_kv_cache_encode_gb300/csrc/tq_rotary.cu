@@ -7,8 +7,9 @@
 // reads the cosines and sines of its pairs once for all of them.
 //
 // 32768 tokens x 64 heads of bf16: 165 us, 0.99 of what a copy of the rows takes (scalar
-// products 211, two-wide ones 197, addresses by steps and three CTAs an SM 166); one token
-// of 64 sequences, 32 heads: 2.8 us, of which the launch is the most.
+// products 211, two-wide ones 197, addresses by steps and three CTAs an SM 166, whose 80
+// registers cost the 16-bit wide variants 16 to 20 bytes of spills); one token of 64 sequences, 32
+// heads: 2.8 us, of which the launch is the most.
 #include <cuda_runtime.h>
 
 #include "tq_decode_impl.cuh"
